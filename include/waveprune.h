@@ -434,6 +434,212 @@ int wp_decode_static(const void *q, const void *kcache, const void *vcache, cons
                      void *stream);
 
 /*
+ * wp_cutoffs_partial — wp_cutoffs for a model that rotates only the first
+ * rot_dim dims of each head: f_c = theta^(-2c/rot_dim), c < rot_dim/2. A dim
+ * from rot_dim on carries no position, so it has no period and is never
+ * masked: a group that holds one has the cutoff WP_CUTOFF_INF.
+ *   rot_dim      a multiple of 16, 16..d_h; rot_dim = d_h gives wp_cutoffs.
+ *   freq_scale, chan_cut  [rot_dim/2]; group_cut [d_h/16]; half-split pairs
+ *                are (c, c + rot_dim/2).
+ * Everything else, and the errors, as in wp_cutoffs.
+ */
+int wp_cutoffs_partial(int d_h, int rot_dim, double theta, const double *freq_scale, double scale_all, double alpha,
+                       int layout, int32_t *chan_cut, int32_t *group_cut);
+
+/*
+ * wp_rope_scaling — frequency scales for a context `factor` times the
+ * original one, host only: a channel that makes at least turns_fast whole
+ * turns over original_len positions keeps its frequency (scale 1), one that
+ * makes at most turns_slow is slowed to 1/factor, a linear ramp in the number
+ * of turns between. *amplitude = 0.1 ln(factor) + 1, the factor on rotated Q
+ * and K that keeps the softmax's sharpness over the longer context.
+ *   rot_dim      multiple of 16, 16..1024; freq_scale out [rot_dim/2].
+ *   factor >= 1, original_len > 0, 0 <= turns_slow < turns_fast (1 and 32 are
+ *   usual).
+ * The cutoffs follow the scaled frequencies: pass the same freq_scale to
+ * wp_cutoffs / wp_cutoffs_partial. Errors: WP_ERR_ARG.
+ */
+int wp_rope_scaling(int rot_dim, double theta, double factor, int original_len, double turns_slow, double turns_fast,
+                    double *freq_scale, double *amplitude);
+
+/*
+ * A strided bf16 tensor [B, N, H, d_h] (strides in elements, dims contiguous):
+ * 16-byte aligned base, strides >= 0 and multiples of 8 (a stride over a size
+ * of 1 is ignored). Slices of one fused Q/K/V projection are such tensors.
+ */
+typedef struct {
+    void *data;
+    int64_t stride_b, stride_n, stride_h;
+} wp_rows;
+
+/*
+ * wp_rope_qk — rotate Q and K in one launch, forward or inverse.
+ *   q, q_out     [B, N, H_q, d_h]; k, k_out [B, N, H_k, d_h]. H_q = 0 or
+ *                H_k = 0 leaves that side out (its pointers are not read).
+ *                An output may be its own input (same base and strides,
+ *                except WP_ROPE_HALF_SPLIT_PAIRED); any other overlap of an
+ *                output with an input or output is WP_ERR_ARG. Inputs may be
+ *                broadcast (stride 0), outputs may not.
+ *   rot_dim      the first rot_dim dims of each head rotate (a multiple of
+ *                16, 16..d_h), the others are copied; f_c = theta^(-2c/rot_dim).
+ *   pos          device int32 [B, N], or NULL: position = pos0 + n.
+ *   amplitude    factor of the rotated dims (1 = plain).
+ *   layout       WP_ROPE_INTERLEAVED (2c, 2c+1), WP_ROPE_HALF_SPLIT
+ *                (c, c + rot_dim/2), or WP_ROPE_HALF_SPLIT_PAIRED, which reads
+ *                half-split and writes interleaved pairs.
+ *   inverse      0: y = amplitude R x. Not 0: y = amplitude R^T x, the gradient
+ *                with respect to x of a forward call with the same arguments
+ *                (paired: reads interleaved pairs, writes half-split).
+ * Angles are formed and reduced modulo 2 pi in fp64, the rotation is fp32,
+ * the result rounds to bf16 once. d_h in {64, 128}.
+ * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED (also: more than 65535 heads or
+ * 2^31-1 tokens), WP_ERR_CUDA.
+ */
+int wp_rope_qk(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_rows *k, const wp_rows *k_out, int H_k, int B,
+               int N, int d_h, int rot_dim, const int32_t *pos, int pos0, double theta, const double *freq_scale,
+               double scale_all, double amplitude, int layout, int inverse, void *stream);
+
+/*
+ * wp_rope_append — rotate the new tokens of a batch and place them in a
+ * cache: q_out = rotated Q, the K row of token i (rotated) and its V row (as
+ * it is) go to key slot[i] of sequence seq[i].
+ *   q, q_out     [T, H_q, d_h] (stride_b ignored), or H_q = 0: K and V only.
+ *   k, v         [T, H_kv, d_h].
+ *   pos, seq, slot  device int32 [T]. A drafted tree has slot = len + node,
+ *                pos = len + depth. seq[i] = -1 marks padding. A token whose
+ *                sequence is outside [0, B), slot outside the cache's
+ *                capacity, or page outside the pool writes nothing to the
+ *                cache (its q_out row is still written). Two tokens must not
+ *                name the same slot.
+ *   kcache, k_layout, vcache  WP_KCACHE_ROWS or WP_KCACHE_GROUP_MAJOR (a
+ *                windowed cache has its own append: WP_ERR_UNSUPPORTED).
+ *   block_table  NULL: contiguous caches [B, H_kv, Lmax, d_h] (group-major K
+ *                [B, H_kv, d_h/16, Lmax, 16]). Otherwise device int32
+ *                [B, max_pages] into pools of n_pages pages of page_size
+ *                keys, as in wp_decode_paged (Lmax is ignored).
+ *   rotation     as in wp_rope_qk; q_out and the cache take the layout's
+ *                output order. q_out may be q (not with the paired layout);
+ *                the caches overlap nothing.
+ * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
+ */
+int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_rows *k, const wp_rows *v, int H_kv, int T,
+                   int d_h, int rot_dim, const int32_t *pos, const int32_t *seq, const int32_t *slot, void *kcache,
+                   int k_layout, void *vcache, int B, int Lmax, const int32_t *block_table, int max_pages,
+                   int page_size, int n_pages, double theta, const double *freq_scale, double scale_all,
+                   double amplitude, int layout, void *stream);
+
+/* wp_decode_tree_workspace_bytes — size of the scratch that wp_decode_tree
+ * needs; Lmax is the cache's capacity per sequence (paged: max_pages *
+ * page_size). 0 on bad arguments. */
+size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, int Lmax);
+
+/*
+ * wp_decode_tree — attention of a tree of drafted tokens over a cache, grouped
+ * cutoffs: the verification step of speculative decoding. Node t of sequence
+ * b stands at position lens[b] + depth(t); its K/V rows are key lens[b] + t of
+ * the cache (wp_rope_append puts them there). It attends the context keys
+ * 0..lens[b]-1, its ancestors and itself; the distance of a pair, which the
+ * cutoffs are compared with, is the difference of the two positions. One
+ * chain (parents t-1) is plain decoding of T tokens; T = 1 with parent -1 is
+ * wp_decode at length lens[b] + 1.
+ *   q            device bf16 [B, T, H_q, d_h], rotated at its positions.
+ *   lens         device int32 [B], 0 or more context keys.
+ *   parents      device int32 [B, T]: parents[b][t] in -1..t-1; -1 = follows
+ *                the context (several roots are fine).
+ *   n_nodes      device int32 [B], 0..T nodes of each sequence, or NULL: T.
+ *                Rows t >= n_nodes[b] of o are 0 and of lse -inf; their q and
+ *                parents are not used.
+ *   kcache, k_layout, vcache, block_table, ...  as in wp_rope_append; read
+ *                only. Keys from lens[b] + n_nodes[b] on may hold anything; the
+ *                V rows below that have to be finite.
+ *   group_cut    host [d_h/16], or NULL: dense.
+ *   o            device bf16 out [B, T, H_q, d_h]; lse device fp32 out
+ *                [B, H_q, T] (natural log, scale included), or NULL.
+ *   workspace    device scratch, 256-byte aligned; contents on entry do not
+ *                matter.
+ * A sequence whose length, node count, parents or pages are out of range gets
+ * NaN rows (nothing is read through them). A wait that gives up records
+ * WP_ERR_TIMEOUT (wp_device_status) and gives NaN rows.
+ * d_h in {64, 128}; T <= 64; H_q/H_kv <= 16. Errors: WP_ERR_ARG,
+ * WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
+ */
+int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *vcache, const int32_t *lens,
+                   const int32_t *parents, const int32_t *n_nodes, int T, int Lmax, const int32_t *block_table,
+                   int max_pages, int page_size, int n_pages, int B, int H_q, int H_kv, int d_h,
+                   const int32_t *group_cut, float softmax_scale, void *o, float *lse, void *workspace,
+                   size_t ws_bytes, void *stream);
+
+/*
+ * wp_kv_compact — keep the accepted path of a drafted tree: the K/V rows of
+ * key lens[b] + path[b][i] move to key lens[b] + i, i < n_keep[b], in place,
+ * and lens_out[b] = lens[b] + n_keep[b]. A node of depth i stands at position
+ * lens[b] + i, so the rows need no new rotation.
+ *   path         device int32 [B, A], strictly increasing within n_keep[b]
+ *                entries (a root-to-leaf path is, since a parent comes before
+ *                its children); n_keep device int32 [B], 0..A.
+ *   lens_out     device int32 [B]; may be lens.
+ *   cache        as in wp_rope_append. The pages written must not be shared
+ *                with another sequence (wp_pages_update sees to it).
+ * A sequence with a bad length, path or page is left as it was, and its
+ * lens_out is -1. A <= 1024. Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
+ */
+int wp_kv_compact(void *kcache, int k_layout, void *vcache, const int32_t *lens, const int32_t *path, int A,
+                  const int32_t *n_keep, int32_t *lens_out, int Lmax, const int32_t *block_table, int max_pages,
+                  int page_size, int n_pages, int B, int H_kv, int d_h, void *stream);
+
+/* info[0] of wp_pages_update. */
+enum { WP_PAGES_OK = 0, WP_PAGES_SHORT = 1, WP_PAGES_BAD_ARGUMENT = 2 };
+
+/* wp_pages_update_workspace_bytes — scratch of wp_pages_update; 0 on bad arguments. */
+size_t wp_pages_update_workspace_bytes(int B, int n_pages);
+
+/*
+ * wp_pages_update — one transaction on the pages of a batch: fork, grow, copy
+ * on write, shrink and free, in one launch and without the host.
+ * Row b of the new batch goes on from row parent[b] of the old one: it keeps
+ * that row's first keep[b] tokens and gets room for new_lens[b] tokens.
+ *   go on: parent = b; fork: parent = another row; free: keep = new_lens = 0.
+ *   - Every old row gives up its ceil(lens/page_size) pages, every new row
+ *     takes up the first ceil(keep/page_size) pages of its parent row.
+ *   - Slots keep .. new_lens-1 will be written. If they begin in a partly
+ *     filled page that has other holders, the row gets a page of its own and
+ *     an entry in `copies`; where all holders are such rows, the lowest one
+ *     keeps the page.
+ *   - Then rows in ascending order take the lowest free pages (count 0).
+ *   refs         device int32 [n_pages]: holders of each page (block tables,
+ *                and whatever else the caller counts), >= 0.
+ *   block_table  device int32 [B, max_pages]; lens, parent, keep, new_lens
+ *                device int32 [B], 0 <= keep[b] <= lens[parent[b]] (parent is
+ *                not read where keep is 0), keep <= new_lens <= capacity.
+ *   refs_out, block_table_out (unused entries -1), lens_out [B] (= new_lens).
+ *   copies       device int32 out [B, 3]: source page, target page, rows to
+ *                copy; (-1, -1, 0) where row b copies nothing. wp_pages_copy
+ *                takes it, once for every layer's pools.
+ *   info         device int32 out [4]: WP_PAGES_*, pages taken (or that would
+ *                have been), free pages there were, copies.
+ * If the free pages do not suffice (WP_PAGES_SHORT) or an entry is out of
+ * range (WP_PAGES_BAD_ARGUMENT), nothing changes: the outputs are the inputs
+ * and copies is empty. No output overlaps an input, another output or the
+ * workspace (4-byte aligned; contents on entry do not matter).
+ * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED (capacity above 2^30), WP_ERR_CUDA.
+ */
+int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32_t *lens, const int32_t *parent,
+                    const int32_t *keep, const int32_t *new_lens, int32_t *refs_out, int32_t *block_table_out,
+                    int32_t *lens_out, int32_t *copies, int32_t *info, int B, int max_pages, int page_size, int n_pages,
+                    void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * wp_pages_copy — copy rows between pages of a K and a V pool (laid out as in
+ * wp_decode_paged): copies device int32 [n, 3], each the source page, the
+ * target page and the number of rows from the page's start, for every KV
+ * head. An entry with a page outside the pool, rows outside 1..page_size, or
+ * source = target copies nothing. A target page must not appear in another
+ * entry. Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
+ */
+int wp_pages_copy(void *k_pages, int k_layout, void *v_pages, const int32_t *copies, int n, int n_pages, int page_size,
+                  int H_kv, int d_h, void *stream);
+
+/*
  * wp_device_status — synchronises `stream`, then reads and clears the device
  * status word of the current device. Returns WP_OK, WP_ERR_TIMEOUT (a kernel
  * gave up waiting since the last call), WP_ERR_ARG (a packed prefill met

@@ -20,6 +20,11 @@ import os
 import numpy as np
 import torch
 
+from . import serving as _serving
+from .serving import (PAGES_BAD_ARGUMENT, PAGES_OK, PAGES_SHORT, TREE_MAX_NODES, wp_cutoffs_partial, wp_decode_tree,
+                      wp_decode_tree_workspace_bytes, wp_kv_compact, wp_pages_copy, wp_pages_update, wp_rope_append,
+                      wp_rope_qk, wp_rope_scaling)
+
 __all__ = [
     "ROPE_INTERLEAVED", "ROPE_HALF_SPLIT", "ROPE_HALF_SPLIT_PAIRED", "MODE_GROUPED", "MODE_CHANNEL", "CUTOFF_INF",
     "WavePruneError", "library_path", "load_library",
@@ -28,6 +33,9 @@ __all__ = [
     "wp_decode_static", "DECODE_STATIC_SCRATCH_BYTES", "wp_kcache_group_major", "KCACHE_ROWS", "KCACHE_GROUP_MAJOR",
     "KCACHE_WINDOWED", "wp_kcache_windowed_elems", "wp_kcache_windowed", "wp_kcache_windowed_append",
     "wp_decode_paged",
+    "wp_cutoffs_partial", "wp_rope_scaling", "wp_rope_qk", "wp_rope_append", "wp_decode_tree",
+    "wp_decode_tree_workspace_bytes", "wp_kv_compact", "wp_pages_update", "wp_pages_copy", "PAGES_OK", "PAGES_SHORT",
+    "PAGES_BAD_ARGUMENT", "TREE_MAX_NODES",
     "wp_device_status", "wp_set_wait_limit", "wp_wait_probe", "wp_status_str",
 ]
 
@@ -109,6 +117,7 @@ def load_library():
     lib.wp_wait_probe.argtypes = [P]
     lib.wp_status_str.restype = ctypes.c_char_p
     lib.wp_status_str.argtypes = [I]
+    _serving.declare(lib)
     _lib = lib
     return lib
 
