@@ -15,6 +15,7 @@
 #include "wp_device.cuh"
 #include "wp_prefill.h"
 #include "wp_rope.h"
+#include "wp_serve.h"
 #include "wp_tile.h"
 
 namespace wp {
@@ -95,6 +96,18 @@ __global__ void wait_probe_kernel(long long limit) {
 }
 
 }  // namespace
+
+long long wait_limit() { return g_wait_limit; }
+
+bool encode_map_4d(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                   const cuuint32_t (&box)[4], CUtensorMapSwizzle sw, CUtensorMapL2promotion promotion) {
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace wp
 
 using namespace wp;

@@ -2,12 +2,18 @@
 // compaction and page kernels (not part of the C ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
 
 namespace wp {
+
+// Defined beside the other calls' tensor maps and wait limit.
+long long wait_limit();
+bool encode_map_4d(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
+                   const cuuint32_t (&box)[4], CUtensorMapSwizzle sw, CUtensorMapL2promotion promotion);
 
 // A K/V cache, contiguous or paged. Both are pools of pages of page_size keys:
 // K [n_pages, Hkv, page_size, D] or (group-major) [n_pages, Hkv, D/16,
@@ -92,17 +98,44 @@ struct PagesCopyArgs {
 cudaError_t launch_pages_copy(const PagesCopyArgs &a, cudaStream_t stream);
 
 constexpr int TREE_MAX_NODES = 64;
+constexpr int TREE_MAX_GROUP = 16;  // query heads per KV head
 
 struct TreeArgs {
-  const __nv_bfloat16 *q;  // [B, T, Hq, D]
   CacheGeom cache;
   const int32_t *lens, *parents, *n_nodes;  // [B], [B, T], [B] or null
   __nv_bfloat16 *o;                         // [B, T, Hq, D]
   float *lse;                               // [B, Hq, T] or null
+  float *o_part, *lse_part;                 // [B, Hkv, T * R, nsplit(, D)], lse base 2
   int B, T, Hq;
+  int tile_nodes, row_tiles;                // nodes per CTA, CTAs per KV head and split
+  int nsplit, box_rows;                     // splits of the keys; rows of one TMA box
   int32_t cut[8];
   float scale_log2;
+  long long wait_limit;
 };
-cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream);
+
+// How the work is cut. Nodes per CTA: as many whole nodes (R rows each) as 128
+// rows hold. Splits: one batch entry fills the 148 SMs x 2 CTAs once, since
+// its splits are equal; several entries have lengths of their own, so their
+// CTAs are cut to fill them about four times over and the SMs even out.
+inline int tree_tile_nodes(int T, int R) { return T < 128 / R ? T : 128 / R; }
+inline int tree_splits(int B, int T, int Hkv, int R, int64_t capacity) {
+  const int tile = tree_tile_nodes(T, R), tiles = (T + tile - 1) / tile;
+  const int64_t units = static_cast<int64_t>(B) * Hkv * tiles;
+  const int64_t want = (B == 1 ? 296 : 4 * 296) / units;
+  const int64_t most = (capacity + 255) / 256;
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+inline size_t tree_partial_o_bytes(int B, int T, int Hq, int nsplit, int D) {
+  return (static_cast<size_t>(B) * T * Hq * nsplit * D * sizeof(float) + 255) & ~static_cast<size_t>(255);
+}
+inline size_t tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t capacity) {
+  const int nsplit = tree_splits(B, T, Hkv, Hq / Hkv, capacity);
+  if (nsplit == 1) return 256;
+  return tree_partial_o_bytes(B, T, Hq, nsplit, D) + static_cast<size_t>(B) * T * Hq * nsplit * sizeof(float);
+}
+cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs &a,
+                        cudaStream_t stream);
 
 }  // namespace wp

@@ -274,7 +274,8 @@ int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_row
 
 size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, int Lmax) {
   if (B <= 0 || T <= 0 || T > TREE_MAX_NODES || H_q <= 0 || H_kv <= 0 || d_h <= 0 || Lmax <= 0) return 0;
-  return 256;
+  if (H_q % H_kv != 0 || H_q / H_kv > TREE_MAX_GROUP) return 0;
+  return tree_workspace_bytes(B, T, H_q, H_kv, d_h, Lmax);
 }
 
 int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *vcache, const int32_t *lens,
@@ -293,14 +294,14 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
                             max_pages, page_size, n_pages, H_kv, d_h, &a.cache);
   if (rc != WP_OK) return rc;
   if (H_q % H_kv != 0 || !std::isfinite(softmax_scale)) return WP_ERR_ARG;
-  if (T > TREE_MAX_NODES || H_q / H_kv > 16) return WP_ERR_UNSUPPORTED;
+  if (T > TREE_MAX_NODES || H_q / H_kv > TREE_MAX_GROUP) return WP_ERR_UNSUPPORTED;
   const int64_t cap = cache_capacity(a.cache);
   if (ws_bytes < wp_decode_tree_workspace_bytes(B, T, H_q, H_kv, d_h, static_cast<int>(cap))) return WP_ERR_ARG;
   for (int g = 0; g < 8; ++g) {
     a.cut[g] = (group_cut == nullptr || g >= d_h / 16) ? WP_CUTOFF_INF : group_cut[g];
     if (a.cut[g] < 0) return WP_ERR_ARG;
   }
-  a.q = static_cast<const __nv_bfloat16 *>(q);
+  const int R = H_q / H_kv, D = d_h;
   a.lens = lens;
   a.parents = parents;
   a.n_nodes = n_nodes;
@@ -309,9 +310,35 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
   a.B = B;
   a.T = T;
   a.Hq = H_q;
+  a.tile_nodes = tree_tile_nodes(T, R);
+  a.row_tiles = (T + a.tile_nodes - 1) / a.tile_nodes;
+  a.nsplit = tree_splits(B, T, H_kv, R, cap);
+  a.box_rows = block_table == nullptr || page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+  a.o_part = static_cast<float *>(workspace);
+  a.lse_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + tree_partial_o_bytes(B, T, H_q, a.nsplit, D));
+  a.wait_limit = wait_limit();
   const float scale = softmax_scale > 0.f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(double(d_h)));
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
-  return from_cuda(launch_tree(a, static_cast<cudaStream_t>(stream)));
+  // Q [B, T, Hq, D]: 16 dims of the R heads of tile_nodes nodes per box. V (and
+  // K in rows) [pages, Hkv, P, D]: 64 dims of box_rows keys. Group-major K
+  // [pages, Hkv * G, P, 16]: one group of box_rows keys. Nothing is promoted
+  // beyond what a box of K needs: its neighbours in memory may be out of window.
+  using U64 = cuuint64_t;
+  using U32 = cuuint32_t;
+  const CacheGeom &g = a.cache;
+  const U64 P = g.page_size, H = H_kv, n = g.n_pages, G = D / 16, row = 2 * D;
+  const U32 box = a.box_rows;
+  CUtensorMap tq, tk, tv;
+  bool ok = encode_map_4d(&tq, q, {U64(D), U64(H_q), U64(T), U64(B)}, {row, row * H_q, row * H_q * T},
+                          {16, U32(R), U32(a.tile_nodes), 1}, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  ok = ok && encode_map_4d(&tv, vcache, {U64(D), P, H, n}, {row, row * P, row * P * H}, {64, box, 1, 1},
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  ok = ok && (g.k_group_major ? encode_map_4d(&tk, kcache, {16, P, H * G, n}, {32, 32 * P, row * P * H}, {16, box, 1, 1},
+                                              CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B)
+                              : encode_map_4d(&tk, kcache, {U64(D), P, H, n}, {row, row * P, row * P * H}, {64, box, 1, 1},
+                                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B));
+  if (!ok) return WP_ERR_CUDA;
+  return from_cuda(launch_tree(tq, tk, tv, a, static_cast<cudaStream_t>(stream)));
 }
 
 int wp_kv_compact(void *kcache, int k_layout, void *vcache, const int32_t *lens, const int32_t *path, int A,

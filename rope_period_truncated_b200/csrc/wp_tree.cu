@@ -1,94 +1,652 @@
-// Attention of a tree of drafted tokens over a cache (simple form: one warp
-// per node and query head).
+// Attention of a tree of drafted tokens over a cache, on sm_100a: TMA +
+// tcgen05 + TMEM, split over the keys.
 //
 // Node t of sequence b stands at position len + depth(t) and sees the keys
-// 0..len-1 of the context, its ancestors and itself (node u's K/V row is slot
+// 0..len-1 of the context, its ancestors and itself (node u's K/V row is key
 // len + u of the cache, at position len + depth(u)):
 //   s_tj = scale * sum_{g : dist <= W_g} q_t[g] . k_j[g],  dist = pos_t - pos_j,
-// then softmax over the visible keys and O = sum_j p_j v_j.
+// then softmax over the visible keys and O = sum_j p_j v_j. A group out of
+// window adds 0; an invisible key is left out of the softmax.
+//
+// The rows of one KV head are its R = Hq/Hkv query heads of every node, row
+// m = node * R + head: they share every K/V tile. One CTA takes up to 128 rows
+// (whole nodes) and one range of keys, in sub-tiles of 64:
+//   warp 4    TMA producer: Q once; per sub-tile the K pieces that a live
+//             group needs (group-major K: one 16-dim box per group; K in rows:
+//             64-dim boxes, four groups each) and V. A box never crosses a
+//             page: it has gcd(page size, 64) rows.
+//   warp 5    issuer: S = sum of one M128 N64 K16 product per live group, O +=
+//             P V (P bf16 in TMEM, V MN-major). S has two 64-column halves, so
+//             the softmax of u runs beside the products of u + 1.
+//   warps 0-3 softmax, a row per thread, online in base 2; O is rescaled only
+//             when a maximum grows by more than 2^8.
+// Groups whose cutoff falls inside a sub-tile's distances go first, one cutoff
+// at a time in ascending order, and S is masked in place after each (windows
+// of ascending cutoffs are nested, so later masks keep what earlier ones did).
+//
+// Sub-tiles that hold drafted keys are the last one or two: there a row takes
+// a 64-bit word of what it sees (context keys, its ancestors' bits), and rows
+// of V behind the last key are zeroed in shared memory before the product, so
+// that P = 0 meets no NaN that an unused slot may hold.
+//
+// Splits write O (fp32) and LSE to the workspace; a second kernel merges them.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
 
 #include "wp_device.cuh"
+#include "wp_prefill_common.cuh"
 #include "wp_serve.h"
 
 namespace wp {
 namespace {
 
-constexpr int WARPS = 4;
+constexpr int SUB = 64;  // keys per sub-tile
+constexpr int KST = 2, VST = 2;
+constexpr int NTHREADS = 192;
+constexpr int PRODUCER_WARP = 4, MMA_WARP = 5;
+constexpr uint32_t TMEM_COLS = 256;  // two CTAs per SM share 512
+constexpr uint32_t COL_S = 0, COL_O = 128;
+constexpr uint32_t Q_TILE = 128 * 32;  // 128 rows x 16 bf16
+constexpr uint32_t K_TILE = SUB * 32;  // 64 keys x 16 bf16 (group-major K)
+constexpr uint32_t CHUNK = SUB * 128;  // 64 keys x 64 bf16 (V, and K in rows)
 
 template <int D>
-__global__ void __launch_bounds__(WARPS * 32) tree_simple_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int E = D / 32;  // dims per lane, all of one group
-  __shared__ int32_t par[TREE_MAX_NODES], depth[TREE_MAX_NODES];
-  const int b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int len = a.lens[b], n = a.n_nodes != nullptr ? a.n_nodes[b] : a.T;
-  const CacheGeom &g = a.cache;
-  bool bad = len < 0 || n < 0 || n > a.T || static_cast<int64_t>(len) + n > cache_capacity(g);
-  if (!bad && threadIdx.x < n) {
-    par[threadIdx.x] = a.parents[static_cast<int64_t>(b) * a.T + threadIdx.x];
-    bad = par[threadIdx.x] < -1 || par[threadIdx.x] >= static_cast<int>(threadIdx.x);
+struct Layout {
+  static constexpr int G = D / 16;
+  static constexpr uint32_t Q_OFF = 0;
+  static constexpr uint32_t K_OFF = G * Q_TILE;
+  static constexpr uint32_t K_STAGE = SUB * D * 2;
+  static constexpr uint32_t V_OFF = K_OFF + KST * K_STAGE;
+  static constexpr uint32_t V_STAGE = SUB * D * 2;
+  static constexpr uint32_t NODE_OFF = V_OFF + VST * V_STAGE;     // uint64 sees[64], int32 depth[64], jump[64]
+  static constexpr uint32_t BAR_OFF = NODE_OFF + 64 * 16;
+  static constexpr uint32_t NUM_BARS = 1 + 2 * KST + 2 * VST + 2 + 2 + 5;
+  static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;    // abort flag, TMEM base, deepest node
+  static constexpr uint32_t BYTES = MISC_OFF + 16 + 1024;         // + alignment
+};
+
+struct Plan {
+  int len, n, total, tiles;  // context keys, nodes, keys, sub-tiles
+  bool ok;
+};
+
+__device__ __forceinline__ Plan sequence_plan(const TreeArgs &a, int b) {
+  Plan p;
+  p.len = a.lens[b];
+  p.n = a.n_nodes != nullptr ? a.n_nodes[b] : a.T;
+  p.ok = p.len >= 0 && p.n >= 0 && p.n <= a.T && static_cast<int64_t>(p.len) + p.n <= cache_capacity(a.cache);
+  p.total = p.ok ? p.len + p.n : 0;
+  p.tiles = (p.total + SUB - 1) / SUB;
+  return p;
+}
+
+// Splits of a sequence: at most a.nsplit, each of at least MIN_TILES sub-tiles.
+constexpr int MIN_TILES = 4;
+__device__ __forceinline__ int sequence_splits(const TreeArgs &a, int tiles) {
+  const int most = (tiles + MIN_TILES - 1) / MIN_TILES;
+  return max(1, min(a.nsplit, most));
+}
+
+// Where row `row` (node * R + head) of KV head hk writes.
+__device__ __forceinline__ int64_t out_row(const TreeArgs &a, int b, int hk, int R, int row) {
+  return (static_cast<int64_t>(b) * a.T + row / R) * a.Hq + hk * R + row % R;
+}
+__device__ __forceinline__ float *out_lse(const TreeArgs &a, int b, int hk, int R, int row) {
+  return a.lse == nullptr ? nullptr : a.lse + (static_cast<int64_t>(b) * a.Hq + hk * R + row % R) * a.T + row / R;
+}
+
+// Full and boundary groups of the sub-tile at key k0, one group per lane:
+// bits 0-7 full, 8-15 boundary. Distances of the pairs that count lie in
+// [dmin, dmax]; with drafted keys in the sub-tile dmin is 0.
+__device__ __forceinline__ uint32_t tile_classes(int W, int G, int len, int deepest, int k0, int lane) {
+  const bool drafts = k0 + SUB > len;
+  const int64_t dmin = drafts ? 0 : static_cast<int64_t>(len) - (k0 + SUB - 1);
+  const int64_t dmax = static_cast<int64_t>(len) + deepest - min(k0, len);
+  const bool live = lane < G && dmin <= W;
+  const bool full = live && dmax <= W;
+  return __ballot_sync(FULL, full) | (__ballot_sync(FULL, live && !full) << 8);
+}
+
+// Columns c of su whose bit is clear become `fill`.
+__device__ __forceinline__ void keep_columns(uint32_t (&su)[64], uint64_t bits, uint32_t fill) {
+  const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    if (!(lo & (1u << c))) su[c] = fill;
+    if (!(hi & (1u << c))) su[32 + c] = fill;
   }
-  if (!bad && g.block_table != nullptr)
-    for (int64_t s = static_cast<int64_t>(threadIdx.x) * g.page_size; s < len + n;
-         s += static_cast<int64_t>(WARPS) * 32 * g.page_size)
-      bad = bad || cache_page(g, b, static_cast<int>(s)) < 0;
+}
+
+template <int D, bool KGM>
+__global__ void __launch_bounds__(NTHREADS, 2)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a) {
+  using L = Layout<D>;
+  constexpr int G = L::G;
+  constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, SUB, false, false);
+  constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *sees = reinterpret_cast<uint64_t *>(smem + L::NODE_OFF);
+  int32_t *depth = reinterpret_cast<int32_t *>(smem + L::NODE_OFF + 64 * 8);
+  int32_t *jump = depth + 64;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::BAR_OFF);
+  uint64_t *q_full = bars, *k_full = q_full + 1, *k_empty = k_full + KST, *v_full = k_empty + KST, *v_empty = v_full + VST,
+           *s_ready = v_empty + VST, *p_ready = s_ready + 2, *o_ready = p_ready + 2, *o_final = o_ready + 1,
+           *bnd_ready = o_final + 1, *bnd_done = bnd_ready + 1, *drain = bnd_done + 1;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF + 4);
+  int *s_deepest = reinterpret_cast<int *>(smem + L::MISC_OFF + 8);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const CacheGeom &cg = a.cache;
+  const int R = a.Hq / cg.Hkv;
+  const int mt = static_cast<int>(blockIdx.x) % a.row_tiles, split = static_cast<int>(blockIdx.x) / a.row_tiles;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int row0 = mt * a.tile_nodes * R;                            // first row of this CTA
+  const int rows = min(a.tile_nodes, a.T - mt * a.tile_nodes) * R;  // up to 128
+  const int warps = (rows + 31) / 32;                               // softmax warps with rows
+  const Plan plan = sequence_plan(a, b);
+  const int splits = sequence_splits(a, plan.tiles);
+  if (split >= splits) return;
+  const int t_begin = static_cast<int>(static_cast<int64_t>(plan.tiles) * split / splits);
+  const int nsub_all = static_cast<int>(static_cast<int64_t>(plan.tiles) * (split + 1) / splits) - t_begin;
+  const int k_begin = t_begin * SUB;
+  const int k_end = min(k_begin + nsub_all * SUB, plan.total);
+  const long long lim = a.wait_limit;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    mbar_init(q_full, 1);
+    for (int s = 0; s < KST; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_ready[s], 1);
+      mbar_init(&p_ready[s], warps);
+    }
+    mbar_init(o_ready, 1);
+    mbar_init(o_final, 1);
+    mbar_init(bnd_ready, 1);
+    mbar_init(bnd_done, warps);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  // The nodes: what each one sees (itself and its ancestors) and its depth, by
+  // pointer doubling: after step i a node has joined 2^i of its ancestors.
+  bool bad = !plan.ok;
+  if (warp == PRODUCER_WARP) {
+    int j[2];
+    uint64_t m[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = lane + 32 * e;
+      j[e] = -1;
+      m[e] = t < plan.n ? 1ull << t : 0ull;
+      if (!bad && t < plan.n) {
+        const int p = a.parents[static_cast<int64_t>(b) * a.T + t];
+        if (p < -1 || p >= t)
+          bad = true;
+        else
+          j[e] = p;
+      }
+    }
+    bad = __any_sync(FULL, bad);
+    if (bad) j[0] = j[1] = -1;
+    while (__any_sync(FULL, j[0] >= 0 || j[1] >= 0)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sees[lane + 32 * e] = m[e];
+        jump[lane + 32 * e] = j[e];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (j[e] >= 0) {
+          m[e] |= sees[j[e]];
+          j[e] = jump[j[e]];
+        }
+      __syncwarp();
+    }
+    int deep = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int d = m[e] ? __popcll(m[e]) - 1 : 0;
+      sees[lane + 32 * e] = m[e];
+      depth[lane + 32 * e] = d;
+      deep = max(deep, d);
+    }
+    deep = __reduce_max_sync(FULL, deep);
+    if (lane == 0) *s_deepest = deep;
+  } else if (!bad && cg.block_table != nullptr) {
+    // a page outside the pool spoils this CTA's rows (its loads would return zeros)
+    const int other = threadIdx.x < PRODUCER_WARP * 32 ? threadIdx.x : threadIdx.x - 32;
+    if (k_begin < k_end)
+      for (int64_t j = k_begin / cg.page_size + other; j <= (k_end - 1) / cg.page_size; j += NTHREADS - 32)
+        bad = bad || cache_page(cg, b, static_cast<int>(j * cg.page_size)) < 0;
+  }
+  tc_fence_before();
   bad = __syncthreads_or(bad);
-  if (!bad && threadIdx.x < n) {
-    int e = 0;
-    for (int t = par[threadIdx.x]; t >= 0; t = par[t]) ++e;
-    depth[threadIdx.x] = e;
-  }
-  __syncthreads();
-  const int idx = blockIdx.x * WARPS + warp;  // node * Hq + head
-  if (idx >= a.T * a.Hq) return;
-  const int t = idx / a.Hq, h = idx % a.Hq, hk = h / (a.Hq / g.Hkv);
-  const int64_t row = (static_cast<int64_t>(b) * a.T + t) * a.Hq + h;
-  float *lse = a.lse == nullptr ? nullptr : a.lse + (static_cast<int64_t>(b) * a.Hq + h) * a.T + t;
-  float acc[E];
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  if (!bad && t < n) {
-    uint64_t seen = 0;
-    for (int u = t; u >= 0; u = par[u]) seen |= 1ull << u;
-    const int W = a.cut[lane * E / 16];
-    float q[E];
-    for (int e = 0; e < E; ++e) q[e] = __bfloat162float(a.q[row * D + lane * E + e]);
-    const int64_t pos = static_cast<int64_t>(len) + depth[t];
-    for (int j = 0; j < len + n; ++j) {
-      if (j >= len && !((seen >> (j - len)) & 1)) continue;
-      const int64_t page = cache_page(g, b, j);
-      const int r = j % g.page_size, d0 = lane * E;
-      const int64_t ko = k_offset(g, page, hk, r, d0 & ~7) + (d0 & 7), vo = v_offset(g, page, hk, r, d0 & ~7) + (d0 & 7);
-      const int64_t dist = pos - (j < len ? j : len + depth[j - len]);
-      float s = 0.f;
-      for (int e = 0; e < E; ++e) s += q[e] * __bfloat162float(g.kc[ko + e]);
-      s = dist <= W ? s : 0.f;
-      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s);
-      const float f = exp2f(m - mn), p = exp2f(s - mn);
-      l = l * f + p;
-      for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + p * __bfloat162float(g.vc[vo + e]);
-      m = mn;
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int deepest = *s_deepest;
+  const int nsub = bad ? 0 : nsub_all;
+  const int my_cut = lane < G ? a.cut[lane] : 0;
+
+  if (warp == PRODUCER_WARP) {
+    // ------------------------------------------------------------ producer
+    const int box = a.box_rows, boxes = SUB / box;
+    int k_issued = 0, v_issued = 0;
+    bool ok = true;
+    // Lane i looks up the page of box i % boxes of a sub-tile.
+    const auto page_of = [&](int u) -> int {
+      const int key = k_begin + u * SUB + (lane % boxes) * box;
+      return u < nsub && key < plan.total ? static_cast<int>(cache_page(cg, b, key)) : -1;
+    };
+    const auto row_of = [&](int u) -> int { return (k_begin + u * SUB + (lane % boxes) * box) % cg.page_size; };
+    if (nsub > 0 && lane == 0) {
+      mbar_arrive_expect_tx(q_full, G * 32u * R * a.tile_nodes);
+      for (int g = 0; g < G; ++g)
+        tma_load_4d(smem + L::Q_OFF + g * Q_TILE, &tm_q, q_full, 16 * g, hk * R, mt * a.tile_nodes, b);
+    }
+    __syncwarp();
+    int page_k = page_of(0), page_v = page_k;  // of the next K and V sub-tile
+    const auto load_v = [&](int u) -> bool {
+      const int st = u % VST;
+      const int pg = page_v, row = row_of(u);
+      page_v = page_of(u + 1);
+      if (u >= VST && !warp_wait_idle(&v_empty[st], ((u / VST) - 1) & 1, lim, abort_flag)) return false;
+      const uint32_t have = __ballot_sync(FULL, lane < boxes && pg >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(&v_full[st], __popc(have) * box * D * 2u);
+      __syncwarp();
+      // lane = chunk * boxes + box
+      if (lane < boxes * (D / 64) && pg >= 0) {
+        const int c = lane / boxes, i = lane % boxes;
+        tma_load_4d(smem + L::V_OFF + st * L::V_STAGE + c * CHUNK + i * box * 128, &tm_v, &v_full[st], 64 * c, row, hk, pg);
+      }
+      __syncwarp();
+      ++v_issued;
+      return true;
+    };
+    for (int u = 0; ok && u < nsub; ++u) {
+      const int st = u % KST;
+      const int pg = page_k, row = row_of(u);
+      page_k = page_of(u + 1);
+      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
+      uint32_t need = (cls | (cls >> 8)) & 0xffu;
+      if (!KGM) need = ((need & 0xfu) ? 1u : 0u) | ((need >> 4) ? 2u : 0u);  // 64-dim chunks
+      if (u >= KST && !warp_wait_idle(&k_empty[st], ((u / KST) - 1) & 1, lim, abort_flag)) {
+        ok = false;
+        break;
+      }
+      const uint32_t have = __ballot_sync(FULL, lane < boxes && pg >= 0);
+      if (lane == 0) mbar_arrive_expect_tx(&k_full[st], __popc(have) * __popc(need) * box * (KGM ? 32u : 128u));
+      __syncwarp();
+      if (KGM) {
+        // lane = group * boxes + box, up to 8 x 4
+        const int g = lane / boxes, i = lane % boxes;
+        if (g < G && ((need >> g) & 1u) && pg >= 0)
+          tma_load_4d(smem + L::K_OFF + st * L::K_STAGE + g * K_TILE + i * box * 32, &tm_k, &k_full[st], 0, row, hk * G + g, pg);
+      } else {
+        const int c = lane / boxes, i = lane % boxes;
+        if (c < D / 64 && ((need >> c) & 1u) && pg >= 0)
+          tma_load_4d(smem + L::K_OFF + st * L::K_STAGE + c * CHUNK + i * box * 128, &tm_k, &k_full[st], 64 * c, row, hk, pg);
+      }
+      __syncwarp();
+      ++k_issued;
+      if (u >= 1) ok = load_v(u - 1);
+    }
+    if (ok && nsub > 0) ok = load_v(nsub - 1);
+    // no bulk copy may still be in flight when this CTA's shared memory goes
+    if (nsub > 0) warp_wait_idle(q_full, 0, lim, nullptr);
+    for (int s = 0; s < KST && s < k_issued; ++s) {
+      const int last = s + ((k_issued - 1 - s) / KST) * KST;
+      warp_wait_idle(&k_full[s], (last / KST) & 1, lim, nullptr);
+    }
+    for (int s = 0; s < VST && s < v_issued; ++s) {
+      const int last = s + ((v_issued - 1 - s) / VST) * VST;
+      warp_wait_idle(&v_full[s], (last / VST) & 1, lim, nullptr);
+    }
+  } else if (warp == MMA_WARP) {
+    // -------------------------------------------------------------- issuer
+    const bool leader = elect_one();
+    const uint64_t q_desc = smem_desc(smem_u32(smem + L::Q_OFF), 16, 256, SMEM_SWIZZLE_32B);
+    const uint64_t k_desc = KGM ? smem_desc(smem_u32(smem + L::K_OFF), 16, 256, SMEM_SWIZZLE_32B)
+                                : smem_desc(smem_u32(smem + L::K_OFF), 16, 1024, SMEM_SWIZZLE_128B);
+    // V: dims contiguous (MN-major); 8-key row groups 1024 B, 64-dim chunks CHUNK apart
+    const uint64_t v_desc = smem_desc(smem_u32(smem + L::V_OFF), CHUNK, 1024, SMEM_SWIZZLE_128B);
+    int bnd_cnt = 0;
+    bool ok = nsub > 0 && warp_wait(q_full, 0, lim, abort_flag);
+    const auto issue_groups = [&](uint32_t s_col, uint64_t kst_desc, uint32_t groups, uint32_t acc) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (groups & (1u << g)) {
+          // K in rows: group g is 32 bytes into the 128-byte rows of chunk g / 4
+          const uint32_t koff = KGM ? g * K_TILE : (g / 4) * CHUNK + (g % 4) * 32;
+          umma_ss(s_col, q_desc + g * (Q_TILE >> 4), kst_desc + (koff >> 4), IDESC_QK, acc);
+          acc = 1;
+        }
+    };
+    const auto issue_qk = [&](int u) -> bool {
+      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
+      const int hh = u & 1;
+      const uint32_t s_col = tmem + COL_S + SUB * hh;
+      const uint64_t kst_desc = k_desc + (((u % KST) * L::K_STAGE) >> 4);
+      uint32_t acc = 0;
+      const uint32_t bnd = cls >> 8;
+      if (bnd) {
+        int64_t prev = -1;
+        int32_t W;
+        uint32_t groups;
+        while (next_boundary_class(a.cut, bnd, prev, &W, &groups)) {
+          if (leader) {
+            issue_groups(s_col, kst_desc, groups, acc);
+            umma_commit(bnd_ready);
+          }
+          acc = 1;
+          __syncwarp();
+          if (!warp_wait(bnd_done, bnd_cnt & 1, lim, abort_flag)) return false;
+          tc_fence_after();
+          ++bnd_cnt;
+          prev = W;
+        }
+      }
+      if (leader) {
+        issue_groups(s_col, kst_desc, cls & 0xffu, acc);
+        umma_commit(&s_ready[hh]);
+        umma_commit(&k_empty[u % KST]);
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int u = 0; ok && u < min(2, nsub); ++u) {
+      ok = warp_wait(&k_full[u % KST], (u / KST) & 1, lim, abort_flag);
+      if (ok) {
+        tc_fence_after();
+        ok = issue_qk(u);
+      }
+    }
+    for (int u = 0; ok && u < nsub; ++u) {
+      const int hh = u & 1, vst = u % VST;
+      if (!warp_wait(&v_full[vst], (u / VST) & 1, lim, abort_flag) || !warp_wait(&p_ready[hh], (u >> 1) & 1, lim, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t vst_desc = v_desc + ((vst * L::V_STAGE) >> 4);
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < SUB / 16; ++kk)
+          umma_ts(tmem + COL_O, tmem + COL_S + SUB * hh + kk * 8, vst_desc + kk * (2048 >> 4), IDESC_PV,
+                  (u > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(o_ready);
+        if (u == nsub - 1) umma_commit(o_final);
+        umma_commit(&v_empty[vst]);
+      }
+      __syncwarp();
+      if (u + 2 < nsub) {
+        ok = warp_wait(&k_full[(u + 2) % KST], ((u + 2) / KST) & 1, lim, abort_flag);
+        if (ok) {
+          tc_fence_after();
+          ok = issue_qk(u + 2);
+        }
+      }
+    }
+    // every product must have finished before TMEM is given back
+    if (leader) umma_commit(drain);
+    __syncwarp();
+    warp_wait(drain, 0, lim, nullptr);
+  } else if (warp < warps) {
+    // ------------------------------------------------------------- softmax
+    const int r = warp * 32 + lane;  // row of the tile == TMEM lane
+    const int node = min(row0 + r, a.T * R - 1) / R;
+    const uint64_t my_sees = sees[node];  // 0 for a node that is not there
+    const int64_t pos = static_cast<int64_t>(plan.len) + depth[node];
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t o_addr = lane_addr + COL_O;
+    const float c2 = a.scale_log2;
+    const uint64_t c2x2 = pack_f2(c2, c2);
+    float m_run = -3.4028234663852886e38f, l_run = 0.f;  // base-2 units; finite, so that m - m is 0
+    int bnd_cnt = 0;
+    bool ok = nsub > 0;
+    for (int u = 0; ok && u < nsub; ++u) {
+      const int hh = u & 1;
+      const int k0 = k_begin + u * SUB;
+      const uint32_t s_addr = lane_addr + COL_S + SUB * hh;
+      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k0, lane);
+      const bool drafts = k0 + SUB > plan.len;
+      if (cls >> 8) {
+        int64_t prev = -1;
+        int32_t W;
+        uint32_t groups;
+        while (next_boundary_class(a.cut, cls >> 8, prev, &W, &groups)) {
+          // keys within the window: dist = pos - key position <= W
+          const int64_t first = pos - W - k0;  // first column of the context inside
+          uint64_t keep = first <= 0 ? ~0ull : first >= 64 ? 0ull : ~0ull << first;
+          if (drafts) {
+            const int c0 = max(plan.len - k0, 0);  // first drafted column
+            if (c0 < 64) keep &= (1ull << c0) - 1;
+#pragma unroll 1
+            for (int c = c0; c < 64; ++c) {
+              const int node_c = k0 + c - plan.len;
+              if (node_c < 64 && pos - (plan.len + depth[node_c]) <= W) keep |= 1ull << c;
+            }
+          }
+          ok = warp_wait(bnd_ready, bnd_cnt & 1, lim, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t su[64];
+          tmem_ld64(s_addr, su);
+          keep_columns(su, keep, 0u);
+          tmem_st32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&su[0]));
+          tmem_st32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&su[32]));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bnd_done);
+          ++bnd_cnt;
+          prev = W;
+        }
+        if (!ok) break;
+      }
+      if (!warp_wait(&s_ready[hh], (u >> 1) & 1, lim, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t su[64];
+      load_half(s_addr, cls != 0, su);
+      if (drafts) {
+        // context columns, then the bits of the nodes this row sees
+        const int c0 = plan.len - k0;  // column of node 0
+        const uint64_t ctx = c0 <= 0 ? 0ull : (1ull << c0) - 1;  // c0 < 64 here
+        const uint64_t own = c0 >= 0 ? my_sees << c0 : c0 > -64 ? my_sees >> -c0 : 0ull;
+        keep_columns(su, ctx | own, 0xff800000u);
+      }
+      const float m_half = half_max(su) * c2;
+      if (__any_sync(FULL, m_half > m_run + RESCALE_THRESHOLD)) {
+        const float m_new = fmaxf(m_run, m_half);
+        if (u > 0) {
+          const float alpha = fast_exp2(m_run - m_new);
+          if (!warp_wait(o_ready, (u - 1) & 1, lim, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          scale_cols_f32(o_addr, D / 32, alpha);
+          l_run *= alpha;
+        }
+        m_run = m_new;
+      }
+      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+      exp_half<false>(su, c2x2, m_run, acc, s_addr);
+      float s0, s1, s2, s3, s4, s5, s6, s7;
+      unpack_f2(acc[0], s0, s1);
+      unpack_f2(acc[1], s2, s3);
+      unpack_f2(acc[2], s4, s5);
+      unpack_f2(acc[3], s6, s7);
+      l_run += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
+      tmem_wait_st();
+      if (k0 + SUB > plan.total) {
+        // rows of V behind the last key: unused slots may hold anything
+        if (!warp_wait(&v_full[u % VST], (u / VST) & 1, lim, abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t *v = smem + L::V_OFF + (u % VST) * L::V_STAGE;
+        const int first = plan.total - k0;
+        for (int e = warp * 32 + lane; e < (SUB - first) * (D / 8); e += warps * 32) {
+          const int rr = first + e / (D / 8), p = e % (D / 8);  // 16-byte piece p of row rr; the swizzle stays in the row
+          *reinterpret_cast<uint4 *>(v + (p / 8) * CHUNK + rr * 128 + (p % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_ready[hh]);
+    }
+    const int row = row0 + r;
+    const bool mine = r < rows;
+    const bool there = plan.ok && row / R < plan.n;
+    const int64_t part = ((static_cast<int64_t>(b) * cg.Hkv + hk) * (a.T * R) + row) * a.nsplit + split;
+    const bool done = ok && warp_wait(o_final, 0, lim, abort_flag);
+    if (done) {
+      tc_fence_after();
+      const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+#pragma unroll
+      for (int c4 = 0; c4 < D / 32; ++c4) {
+        uint32_t ov[32];
+        tmem_ld32(o_addr + 32 * c4, ov);
+        tmem_wait_ld(ov);
+        if (!mine) continue;
+        if (a.nsplit > 1) {
+          float4 *dst = reinterpret_cast<float4 *>(a.o_part + part * D + 32 * c4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(__uint_as_float(ov[4 * k]) * inv_l, __uint_as_float(ov[4 * k + 1]) * inv_l,
+                                 __uint_as_float(ov[4 * k + 2]) * inv_l, __uint_as_float(ov[4 * k + 3]) * inv_l);
+        } else {
+          uint4 *dst = reinterpret_cast<uint4 *>(a.o + out_row(a, b, hk, R, row) * D + 32 * c4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (there)
+              w = make_uint4(pack_bf16x2(__uint_as_float(ov[8 * k]) * inv_l, __uint_as_float(ov[8 * k + 1]) * inv_l),
+                             pack_bf16x2(__uint_as_float(ov[8 * k + 2]) * inv_l, __uint_as_float(ov[8 * k + 3]) * inv_l),
+                             pack_bf16x2(__uint_as_float(ov[8 * k + 4]) * inv_l, __uint_as_float(ov[8 * k + 5]) * inv_l),
+                             pack_bf16x2(__uint_as_float(ov[8 * k + 6]) * inv_l, __uint_as_float(ov[8 * k + 7]) * inv_l));
+            dst[k] = w;
+          }
+        }
+      }
+    } else if (nsub > 0) {
+      *abort_flag = 1;
+    }
+    if (mine) {
+      const float lse2 = m_run + __log2f(l_run);  // -inf where no key of this range is visible
+      // not done: no keys at all (every row is empty), or a bad sequence, page or wait: NaN rows
+      const bool spoilt = !done && (bad || nsub > 0);
+      if (a.nsplit > 1) {
+        if (!done && !spoilt)
+          for (int k = 0; k < D; ++k) a.o_part[part * D + k] = 0.f;
+        a.lse_part[part] = spoilt ? INFINITY : done ? lse2 : -INFINITY;
+      } else {
+        if (!done) {
+          const uint32_t w = spoilt ? 0x7FC07FC0u : 0u;
+          uint4 *dst = reinterpret_cast<uint4 *>(a.o + out_row(a, b, hk, R, row) * D);
+          for (int k = 0; k < D / 8; ++k) dst[k] = make_uint4(w, w, w, w);
+        }
+        float *lse = out_lse(a, b, hk, R, row);
+        if (lse != nullptr)
+          *lse = spoilt ? __int_as_float(0x7FC00000) : done && there ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+      }
     }
   }
-  const float nan = __int_as_float(0x7fc00000);
-  for (int e = 0; e < E; ++e)
-    a.o[row * D + lane * E + e] = __float2bfloat16_rn(bad ? nan : t < n ? acc[e] / l : 0.f);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// One warp per row: O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M).
+constexpr int COMBINE_WARPS = 4;
+
+template <int D>
+__global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int E = D / 32;
+  const int R = a.Hq / a.cache.Hkv;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * COMBINE_WARPS + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (id >= static_cast<int64_t>(a.B) * a.T * a.Hq) return;
+  const int row = static_cast<int>(id % (a.T * R));
+  const int hk = static_cast<int>(id / (a.T * R) % a.cache.Hkv);
+  const int b = static_cast<int>(id / (a.T * R) / a.cache.Hkv);
+  const Plan plan = sequence_plan(a, b);
+  const int splits = sequence_splits(a, plan.tiles);
+  const float *lp = a.lse_part + id * a.nsplit;
+  const float *op = a.o_part + id * a.nsplit * D + lane * E;
+  float acc[E], sum = 0.f, M = -INFINITY;
+  bool spoilt = !plan.ok;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  const bool there = plan.ok && row / R < plan.n;
+  if (there) {
+    for (int s = 0; s < splits; ++s) M = fmaxf(M, lp[s]);
+    spoilt = M == INFINITY;
+    for (int s = 0; s < splits; ++s) {
+      const float w = lp[s] == -INFINITY ? 0.f : fast_exp2(lp[s] - M);
+      sum += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * op[static_cast<int64_t>(s) * D + e];
+    }
+  }
+  __nv_bfloat16 *o = a.o + out_row(a, b, hk, R, row) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float x = spoilt ? __int_as_float(0x7fc00000) : there ? acc[e] / sum : 0.f;
+    const float y = spoilt ? __int_as_float(0x7fc00000) : there ? acc[e + 1] / sum : 0.f;
+    *reinterpret_cast<uint32_t *>(o + e) = pack_bf16x2(x, y);
+  }
+  float *lse = out_lse(a, b, hk, R, row);
   if (lane == 0 && lse != nullptr)
-    *lse = bad ? nan : t < n ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    *lse = spoilt ? __int_as_float(0x7fc00000) : there ? (M + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D, bool KGM>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs &a, cudaStream_t stream) {
+  const int smem = static_cast<int>(Layout<D>::BYTES);
+  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, KGM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(a.row_tiles * a.nsplit, a.cache.Hkv, a.B);
+  tree_kernel<D, KGM><<<grid, NTHREADS, smem, stream>>>(tq, tk, tv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.nsplit == 1) return e;
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
+  tree_combine_kernel<D><<<static_cast<unsigned>((rows + COMBINE_WARPS - 1) / COMBINE_WARPS), COMBINE_WARPS * 32, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree(const TreeArgs &a, cudaStream_t stream) {
-  const dim3 grid((a.T * a.Hq + WARPS - 1) / WARPS, a.B);
+cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs &a,
+                        cudaStream_t stream) {
   if (a.cache.D == 128)
-    tree_simple_kernel<128><<<grid, WARPS * 32, 0, stream>>>(a);
-  else
-    tree_simple_kernel<64><<<grid, WARPS * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+    return a.cache.k_group_major ? launch<128, true>(tq, tk, tv, a, stream) : launch<128, false>(tq, tk, tv, a, stream);
+  return a.cache.k_group_major ? launch<64, true>(tq, tk, tv, a, stream) : launch<64, false>(tq, tk, tv, a, stream);
 }
 
 }  // namespace wp
