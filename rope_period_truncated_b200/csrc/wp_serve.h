@@ -98,6 +98,7 @@ struct PagesCopyArgs {
 cudaError_t launch_pages_copy(const PagesCopyArgs &a, cudaStream_t stream);
 
 constexpr int TREE_MAX_NODES = 64;
+constexpr int TREE_MAX_STAGES = 6;  // of K and of V
 constexpr int TREE_MAX_GROUP = 16;  // query heads per KV head
 
 struct TreeArgs {
@@ -109,6 +110,7 @@ struct TreeArgs {
   int B, T, Hq;
   int tile_nodes, row_tiles;                // nodes per CTA, CTAs per KV head and split
   int nsplit, box_rows;                     // splits of the keys; rows of one TMA box
+  int k_stages, v_stages;                   // ring depths, set at the launch
   int32_t cut[8];
   float scale_log2;
   long long wait_limit;

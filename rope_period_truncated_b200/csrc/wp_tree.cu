@@ -42,28 +42,46 @@ namespace wp {
 namespace {
 
 constexpr int SUB = 64;  // keys per sub-tile
-constexpr int KST = 2, VST = 2;
 constexpr int NTHREADS = 192;
 constexpr int PRODUCER_WARP = 4, MMA_WARP = 5;
+constexpr int SMEM_PER_CTA = 115712;  // (228 KB - 2 x 1 KB reserved) / 2
 constexpr uint32_t TMEM_COLS = 256;  // two CTAs per SM share 512
 constexpr uint32_t COL_S = 0, COL_O = 128;
-constexpr uint32_t Q_TILE = 128 * 32;  // 128 rows x 16 bf16
 constexpr uint32_t K_TILE = SUB * 32;  // 64 keys x 16 bf16 (group-major K)
 constexpr uint32_t CHUNK = SUB * 128;  // 64 keys x 64 bf16 (V, and K in rows)
+
+// Shared memory: the K and V rings, then Q (one tile of `rows` rows per group,
+// rows rounded up to 8), then the nodes and barriers. The products read 128
+// rows from each Q tile: what lies beyond a tile's rows (the next tile, or the
+// space behind the last) only makes rows of S and O that nobody reads.
+constexpr uint32_t NUM_BARS = 1 + 4 * TREE_MAX_STAGES + 2 + 2 + 5;
 
 template <int D>
 struct Layout {
   static constexpr int G = D / 16;
-  static constexpr uint32_t Q_OFF = 0;
-  static constexpr uint32_t K_OFF = G * Q_TILE;
-  static constexpr uint32_t K_STAGE = SUB * D * 2;
-  static constexpr uint32_t V_OFF = K_OFF + KST * K_STAGE;
-  static constexpr uint32_t V_STAGE = SUB * D * 2;
-  static constexpr uint32_t NODE_OFF = V_OFF + VST * V_STAGE;     // uint64 sees[64], int32 depth[64], jump[64]
-  static constexpr uint32_t BAR_OFF = NODE_OFF + 64 * 16;
-  static constexpr uint32_t NUM_BARS = 1 + 2 * KST + 2 * VST + 2 + 2 + 5;
-  static constexpr uint32_t MISC_OFF = BAR_OFF + NUM_BARS * 8;    // abort flag, TMEM base, deepest node
-  static constexpr uint32_t BYTES = MISC_OFF + 16 + 1024;         // + alignment
+  static constexpr uint32_t STAGE = SUB * D * 2;  // one K or V sub-tile
+  uint32_t v_off, q_off, q_tile, node_off, bar_off, misc_off;
+  __host__ __device__ Layout(int kst, int vst, int rows) {
+    v_off = kst * STAGE;
+    q_off = v_off + vst * STAGE;
+    q_tile = ((rows + 7) & ~7) * 32;
+    node_off = q_off + (G - 1) * q_tile + 128 * 32;  // uint64 sees[64], int32 depth[64], jump[64]
+    bar_off = node_off + 64 * 16;
+    misc_off = bar_off + NUM_BARS * 8;  // abort flag, TMEM base, deepest node
+  }
+  __host__ __device__ uint32_t bytes() const { return misc_off + 16 + 1024; }  // + alignment
+};
+
+// Position in a ring of stages: slot, and the parity of its current round.
+struct Ring {
+  int slot = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++slot == stages) {
+      slot = 0;
+      round ^= 1u;
+    }
+  }
 };
 
 struct Plan {
@@ -122,22 +140,24 @@ template <int D, bool KGM>
 __global__ void __launch_bounds__(NTHREADS, 2)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a) {
-  using L = Layout<D>;
-  constexpr int G = L::G;
+  constexpr int G = D / 16;
+  constexpr uint32_t STAGE = Layout<D>::STAGE;
   constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, SUB, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, D, false, true);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *sees = reinterpret_cast<uint64_t *>(smem + L::NODE_OFF);
-  int32_t *depth = reinterpret_cast<int32_t *>(smem + L::NODE_OFF + 64 * 8);
+  const int KST = a.k_stages, VST = a.v_stages;
+  const Layout<D> L(KST, VST, a.tile_nodes * (a.Hq / a.cache.Hkv));
+  uint64_t *sees = reinterpret_cast<uint64_t *>(smem + L.node_off);
+  int32_t *depth = reinterpret_cast<int32_t *>(smem + L.node_off + 64 * 8);
   int32_t *jump = depth + 64;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::BAR_OFF);
-  uint64_t *q_full = bars, *k_full = q_full + 1, *k_empty = k_full + KST, *v_full = k_empty + KST, *v_empty = v_full + VST,
-           *s_ready = v_empty + VST, *p_ready = s_ready + 2, *o_ready = p_ready + 2, *o_final = o_ready + 1,
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bar_off);
+  uint64_t *q_full = bars, *k_full = q_full + 1, *k_empty = k_full + TREE_MAX_STAGES, *v_full = k_empty + TREE_MAX_STAGES,
+           *v_empty = v_full + TREE_MAX_STAGES, *s_ready = v_empty + TREE_MAX_STAGES, *p_ready = s_ready + 2, *o_ready = p_ready + 2, *o_final = o_ready + 1,
            *bnd_ready = o_final + 1, *bnd_done = bnd_ready + 1, *drain = bnd_done + 1;
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::MISC_OFF);
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::MISC_OFF + 4);
-  int *s_deepest = reinterpret_cast<int *>(smem + L::MISC_OFF + 8);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L.misc_off);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L.misc_off + 4);
+  int *s_deepest = reinterpret_cast<int *>(smem + L.misc_off + 8);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const CacheGeom &cg = a.cache;
@@ -240,73 +260,101 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int deepest = *s_deepest;
+  // The rows' place among the 128 lanes. A warp reaches the lanes of its own
+  // quarter only, and warps w of both CTAs of an SM share a scheduler: few rows
+  // go to other quarters in the CTA that got the upper half of TMEM, and one
+  // warp of rows also stays off the schedulers of the producer and the issuer.
+  const int half = (tmem & 0xffffu) >= TMEM_COLS ? 1 : 0;
+  const int warp0 = warps == 1 ? 2 + half : warps == 2 ? 2 * half : 0;
   const int nsub = bad ? 0 : nsub_all;
   const int my_cut = lane < G ? a.cut[lane] : 0;
 
   if (warp == PRODUCER_WARP) {
     // ------------------------------------------------------------ producer
+    // Lane i looks up where box i % boxes of a sub-tile lies, one sub-tile
+    // ahead of its loads (the block table's entry arrives meanwhile); one
+    // elected lane issues every copy, in a warp-uniform loop.
+    const bool leader = elect_one();
     const int box = a.box_rows, boxes = SUB / box;
+    Ring kr, vr;  // of the next K and V load; a slot is free once its previous round was consumed
     int k_issued = 0, v_issued = 0;
     bool ok = true;
-    // Lane i looks up the page of box i % boxes of a sub-tile.
-    const auto page_of = [&](int u) -> int {
-      const int key = k_begin + u * SUB + (lane % boxes) * box;
-      return u < nsub && key < plan.total ? static_cast<int>(cache_page(cg, b, key)) : -1;
+    struct Place {
+      int page, row;  // page < 0: behind the last key, nothing to load
     };
-    const auto row_of = [&](int u) -> int { return (k_begin + u * SUB + (lane % boxes) * box) % cg.page_size; };
-    if (nsub > 0 && lane == 0) {
+    const auto place_of = [&](int u) -> Place {
+      const int key = k_begin + u * SUB + (lane & (boxes - 1)) * box;
+      Place p{-1, 0};
+      if (u < nsub && key < plan.total) {
+        if (cg.block_table == nullptr) {
+          p = Place{b, key};
+        } else {
+          const int j = key / cg.page_size;
+          p = Place{cg.block_table[static_cast<int64_t>(b) * cg.max_pages + j], key - j * cg.page_size};
+        }
+      }
+      return p;
+    };
+    if (nsub > 0 && leader) {
       mbar_arrive_expect_tx(q_full, G * 32u * R * a.tile_nodes);
       for (int g = 0; g < G; ++g)
-        tma_load_4d(smem + L::Q_OFF + g * Q_TILE, &tm_q, q_full, 16 * g, hk * R, mt * a.tile_nodes, b);
+        tma_load_4d(smem + L.q_off + g * L.q_tile, &tm_q, q_full, 16 * g, hk * R, mt * a.tile_nodes, b);
     }
     __syncwarp();
-    int page_k = page_of(0), page_v = page_k;  // of the next K and V sub-tile
-    const auto load_v = [&](int u) -> bool {
-      const int st = u % VST;
-      const int pg = page_v, row = row_of(u);
-      page_v = page_of(u + 1);
-      if (u >= VST && !warp_wait_idle(&v_empty[st], ((u / VST) - 1) & 1, lim, abort_flag)) return false;
-      const uint32_t have = __ballot_sync(FULL, lane < boxes && pg >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(&v_full[st], __popc(have) * box * D * 2u);
-      __syncwarp();
-      // lane = chunk * boxes + box
-      if (lane < boxes * (D / 64) && pg >= 0) {
-        const int c = lane / boxes, i = lane % boxes;
-        tma_load_4d(smem + L::V_OFF + st * L::V_STAGE + c * CHUNK + i * box * 128, &tm_v, &v_full[st], 64 * c, row, hk, pg);
+    const auto load_v = [&](int u, Place pl) -> bool {
+      const int st = vr.slot;
+      if (u >= VST && !warp_wait_idle(&v_empty[st], vr.round ^ 1u, lim, abort_flag)) return false;
+      const int have = __popc(__ballot_sync(FULL, lane < boxes && pl.page >= 0));
+      if (leader) mbar_arrive_expect_tx(&v_full[st], have * box * D * 2u);
+      uint8_t *dst = smem + L.v_off + st * STAGE;
+      for (int i = 0; i < have; ++i) {  // the boxes that exist come first
+        const int page = __shfl_sync(FULL, pl.page, i), row = __shfl_sync(FULL, pl.row, i);
+        if (leader) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_4d(dst + c * CHUNK + i * box * 128, &tm_v, &v_full[st], 64 * c, row, hk, page);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       ++v_issued;
+      vr.next(VST);
       return true;
     };
+    Place here = place_of(0), before = here;
     for (int u = 0; ok && u < nsub; ++u) {
-      const int st = u % KST;
-      const int pg = page_k, row = row_of(u);
-      page_k = page_of(u + 1);
+      const Place next = place_of(u + 1);
+      const int st = kr.slot;
       const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
       uint32_t need = (cls | (cls >> 8)) & 0xffu;
       if (!KGM) need = ((need & 0xfu) ? 1u : 0u) | ((need >> 4) ? 2u : 0u);  // 64-dim chunks
-      if (u >= KST && !warp_wait_idle(&k_empty[st], ((u / KST) - 1) & 1, lim, abort_flag)) {
+      if (u >= KST && !warp_wait_idle(&k_empty[st], kr.round ^ 1u, lim, abort_flag)) {
         ok = false;
         break;
       }
-      const uint32_t have = __ballot_sync(FULL, lane < boxes && pg >= 0);
-      if (lane == 0) mbar_arrive_expect_tx(&k_full[st], __popc(have) * __popc(need) * box * (KGM ? 32u : 128u));
-      __syncwarp();
-      if (KGM) {
-        // lane = group * boxes + box, up to 8 x 4
-        const int g = lane / boxes, i = lane % boxes;
-        if (g < G && ((need >> g) & 1u) && pg >= 0)
-          tma_load_4d(smem + L::K_OFF + st * L::K_STAGE + g * K_TILE + i * box * 32, &tm_k, &k_full[st], 0, row, hk * G + g, pg);
-      } else {
-        const int c = lane / boxes, i = lane % boxes;
-        if (c < D / 64 && ((need >> c) & 1u) && pg >= 0)
-          tma_load_4d(smem + L::K_OFF + st * L::K_STAGE + c * CHUNK + i * box * 128, &tm_k, &k_full[st], 64 * c, row, hk, pg);
+      const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
+      if (leader) mbar_arrive_expect_tx(&k_full[st], have * __popc(need) * box * (KGM ? 32u : 128u));
+      uint8_t *dst = smem + st * STAGE;
+      for (int i = 0; i < have; ++i) {
+        const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
+        if (leader) {
+#pragma unroll
+          for (int g = 0; g < (KGM ? G : D / 64); ++g)
+            if ((need >> g) & 1u) {
+              if (KGM)
+                tma_load_4d(dst + g * K_TILE + i * box * 32, &tm_k, &k_full[st], 0, row, hk * G + g, page);
+              else
+                tma_load_4d(dst + g * CHUNK + i * box * 128, &tm_k, &k_full[st], 64 * g, row, hk, page);
+            }
+        }
+        __syncwarp();
       }
-      __syncwarp();
       ++k_issued;
-      if (u >= 1) ok = load_v(u - 1);
+      kr.next(KST);
+      if (u >= 1) ok = load_v(u - 1, before);
+      before = here;
+      here = next;
     }
-    if (ok && nsub > 0) ok = load_v(nsub - 1);
+    if (ok && nsub > 0) ok = load_v(nsub - 1, before);
     // no bulk copy may still be in flight when this CTA's shared memory goes
     if (nsub > 0) warp_wait_idle(q_full, 0, lim, nullptr);
     for (int s = 0; s < KST && s < k_issued; ++s) {
@@ -320,11 +368,13 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   } else if (warp == MMA_WARP) {
     // -------------------------------------------------------------- issuer
     const bool leader = elect_one();
-    const uint64_t q_desc = smem_desc(smem_u32(smem + L::Q_OFF), 16, 256, SMEM_SWIZZLE_32B);
-    const uint64_t k_desc = KGM ? smem_desc(smem_u32(smem + L::K_OFF), 16, 256, SMEM_SWIZZLE_32B)
-                                : smem_desc(smem_u32(smem + L::K_OFF), 16, 1024, SMEM_SWIZZLE_128B);
+    // row 0 of Q stands in lane 32 * warp0: the tile begins that many rows earlier
+    const uint64_t q_desc = smem_desc(smem_u32(smem + L.q_off) - warp0 * 1024, 16, 256, SMEM_SWIZZLE_32B);
+    const uint64_t k_desc = KGM ? smem_desc(smem_u32(smem), 16, 256, SMEM_SWIZZLE_32B)
+                                : smem_desc(smem_u32(smem), 16, 1024, SMEM_SWIZZLE_128B);
     // V: dims contiguous (MN-major); 8-key row groups 1024 B, 64-dim chunks CHUNK apart
-    const uint64_t v_desc = smem_desc(smem_u32(smem + L::V_OFF), CHUNK, 1024, SMEM_SWIZZLE_128B);
+    const uint64_t v_desc = smem_desc(smem_u32(smem + L.v_off), CHUNK, 1024, SMEM_SWIZZLE_128B);
+    Ring kr, vr;  // of the next S and P V products
     int bnd_cnt = 0;
     bool ok = nsub > 0 && warp_wait(q_full, 0, lim, abort_flag);
     const auto issue_groups = [&](uint32_t s_col, uint64_t kst_desc, uint32_t groups, uint32_t acc) {
@@ -333,7 +383,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         if (groups & (1u << g)) {
           // K in rows: group g is 32 bytes into the 128-byte rows of chunk g / 4
           const uint32_t koff = KGM ? g * K_TILE : (g / 4) * CHUNK + (g % 4) * 32;
-          umma_ss(s_col, q_desc + g * (Q_TILE >> 4), kst_desc + (koff >> 4), IDESC_QK, acc);
+          umma_ss(s_col, q_desc + g * (L.q_tile >> 4), kst_desc + (koff >> 4), IDESC_QK, acc);
           acc = 1;
         }
     };
@@ -341,7 +391,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
       const int hh = u & 1;
       const uint32_t s_col = tmem + COL_S + SUB * hh;
-      const uint64_t kst_desc = k_desc + (((u % KST) * L::K_STAGE) >> 4);
+      const uint64_t kst_desc = k_desc + ((kr.slot * STAGE) >> 4);
       uint32_t acc = 0;
       const uint32_t bnd = cls >> 8;
       if (bnd) {
@@ -364,26 +414,27 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       if (leader) {
         issue_groups(s_col, kst_desc, cls & 0xffu, acc);
         umma_commit(&s_ready[hh]);
-        umma_commit(&k_empty[u % KST]);
+        umma_commit(&k_empty[kr.slot]);
       }
       __syncwarp();
+      kr.next(KST);
       return true;
     };
     for (int u = 0; ok && u < min(2, nsub); ++u) {
-      ok = warp_wait(&k_full[u % KST], (u / KST) & 1, lim, abort_flag);
+      ok = warp_wait(&k_full[kr.slot], kr.round, lim, abort_flag);
       if (ok) {
         tc_fence_after();
         ok = issue_qk(u);
       }
     }
     for (int u = 0; ok && u < nsub; ++u) {
-      const int hh = u & 1, vst = u % VST;
-      if (!warp_wait(&v_full[vst], (u / VST) & 1, lim, abort_flag) || !warp_wait(&p_ready[hh], (u >> 1) & 1, lim, abort_flag)) {
+      const int hh = u & 1, vst = vr.slot;
+      if (!warp_wait(&v_full[vst], vr.round, lim, abort_flag) || !warp_wait(&p_ready[hh], (u >> 1) & 1, lim, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint64_t vst_desc = v_desc + ((vst * L::V_STAGE) >> 4);
+      const uint64_t vst_desc = v_desc + ((vst * STAGE) >> 4);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < SUB / 16; ++kk)
@@ -394,8 +445,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         umma_commit(&v_empty[vst]);
       }
       __syncwarp();
+      vr.next(VST);
       if (u + 2 < nsub) {
-        ok = warp_wait(&k_full[(u + 2) % KST], ((u + 2) / KST) & 1, lim, abort_flag);
+        ok = warp_wait(&k_full[kr.slot], kr.round, lim, abort_flag);
         if (ok) {
           tc_fence_after();
           ok = issue_qk(u + 2);
@@ -406,9 +458,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     if (leader) umma_commit(drain);
     __syncwarp();
     warp_wait(drain, 0, lim, nullptr);
-  } else if (warp < warps) {
+  } else if (warp >= warp0 && warp < warp0 + warps) {
     // ------------------------------------------------------------- softmax
-    const int r = warp * 32 + lane;  // row of the tile == TMEM lane
+    const int r = (warp - warp0) * 32 + lane;  // row of the tile, in TMEM lane 32 * warp + lane
     const int node = min(row0 + r, a.T * R - 1) / R;
     const uint64_t my_sees = sees[node];  // 0 for a node that is not there
     const int64_t pos = static_cast<int64_t>(plan.len) + depth[node];
@@ -503,9 +555,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           ok = false;
           break;
         }
-        uint8_t *v = smem + L::V_OFF + (u % VST) * L::V_STAGE;
+        uint8_t *v = smem + L.v_off + (u % VST) * STAGE;
         const int first = plan.total - k0;
-        for (int e = warp * 32 + lane; e < (SUB - first) * (D / 8); e += warps * 32) {
+        for (int e = r; e < (SUB - first) * (D / 8); e += warps * 32) {
           const int rr = first + e / (D / 8), p = e % (D / 8);  // 16-byte piece p of row rr; the swizzle stays in the row
           *reinterpret_cast<uint4 *>(v + (p / 8) * CHUNK + rr * 128 + (p % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -627,16 +679,22 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const 
 }
 
 template <int D, bool KGM>
-cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs &a, cudaStream_t stream) {
-  const int smem = static_cast<int>(Layout<D>::BYTES);
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, TreeArgs a, cudaStream_t stream) {
+  // as many stages as let two CTAs share an SM, one more of K than of V where
+  // the number is odd
+  const int rows = a.tile_nodes * (a.Hq / a.cache.Hkv);
+  const int stages = min(2 * TREE_MAX_STAGES, (SMEM_PER_CTA - static_cast<int>(Layout<D>(0, 0, rows).bytes())) / static_cast<int>(Layout<D>::STAGE));
+  a.v_stages = stages / 2;
+  a.k_stages = stages - a.v_stages;
+  const int smem = static_cast<int>(Layout<D>(a.k_stages, a.v_stages, rows).bytes());
   cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, KGM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.row_tiles * a.nsplit, a.cache.Hkv, a.B);
   tree_kernel<D, KGM><<<grid, NTHREADS, smem, stream>>>(tq, tk, tv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.nsplit == 1) return e;
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  tree_combine_kernel<D><<<static_cast<unsigned>((rows + COMBINE_WARPS - 1) / COMBINE_WARPS), COMBINE_WARPS * 32, 0, stream>>>(a);
+  const int64_t all_rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
+  tree_combine_kernel<D><<<static_cast<unsigned>((all_rows + COMBINE_WARPS - 1) / COMBINE_WARPS), COMBINE_WARPS * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
