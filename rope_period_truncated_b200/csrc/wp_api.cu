@@ -99,12 +99,12 @@ __global__ void wait_probe_kernel(long long limit) {
 
 long long wait_limit() { return g_wait_limit; }
 
-bool encode_map_4d(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
-                   const cuuint32_t (&box)[4], CUtensorMapSwizzle sw, CUtensorMapL2promotion promotion) {
+bool encode_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                const cuuint32_t *box, CUtensorMapSwizzle sw, CUtensorMapL2promotion promotion) {
   auto enc = tensor_map_encoder();
   if (enc == nullptr) return false;
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

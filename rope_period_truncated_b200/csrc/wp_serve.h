@@ -12,8 +12,8 @@ namespace wp {
 
 // Defined beside the other calls' tensor maps and wait limit.
 long long wait_limit();
-bool encode_map_4d(CUtensorMap *m, const void *base, const cuuint64_t (&dims)[4], const cuuint64_t (&strides)[3],
-                   const cuuint32_t (&box)[4], CUtensorMapSwizzle sw, CUtensorMapL2promotion promotion);
+bool encode_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                const cuuint32_t *box, CUtensorMapSwizzle sw, CUtensorMapL2promotion promotion);
 
 // A K/V cache, contiguous or paged. Both are pools of pages of page_size keys:
 // K [n_pages, Hkv, page_size, D] or (group-major) [n_pages, Hkv, D/16,
@@ -137,7 +137,13 @@ inline size_t tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t
   if (nsplit == 1) return 256;
   return tree_partial_o_bytes(B, T, Hq, nsplit, D) + static_cast<size_t>(B) * T * Hq * nsplit * sizeof(float);
 }
-cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs &a,
-                        cudaStream_t stream);
+
+// Tensor maps. Q: 16 dims of the R heads of tile_nodes nodes. V: box_rows keys
+// whole. K in boxes of box_rows keys: group-major 1, 2 or 4 groups, in rows 1
+// or 2 chunks of 64 dims.
+struct TreeMaps {
+  CUtensorMap q, v, k[3];
+};
+cudaError_t launch_tree(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream);
 
 }  // namespace wp

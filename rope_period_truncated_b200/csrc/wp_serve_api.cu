@@ -319,26 +319,30 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
   a.wait_limit = wait_limit();
   const float scale = softmax_scale > 0.f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(double(d_h)));
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
-  // Q [B, T, Hq, D]: 16 dims of the R heads of tile_nodes nodes per box. V (and
-  // K in rows) [pages, Hkv, P, D]: 64 dims of box_rows keys. Group-major K
-  // [pages, Hkv * G, P, 16]: one group of box_rows keys. Nothing is promoted
-  // beyond what a box of K needs: its neighbours in memory may be out of window.
-  using U64 = cuuint64_t;
-  using U32 = cuuint32_t;
+  // Q [B, T, Hq, D]; V and K in rows [pages, Hkv, P, D] with the dims as
+  // chunks of 64; group-major K [pages, Hkv, G, P, 16]. K is promoted in L2 no
+  // further than a line: its neighbours in memory may be out of window.
   const CacheGeom &g = a.cache;
-  const U64 P = g.page_size, H = H_kv, n = g.n_pages, G = D / 16, row = 2 * D;
-  const U32 box = a.box_rows;
-  CUtensorMap tq, tk, tv;
-  bool ok = encode_map_4d(&tq, q, {U64(D), U64(H_q), U64(T), U64(B)}, {row, row * H_q, row * H_q * T},
-                          {16, U32(R), U32(a.tile_nodes), 1}, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-  ok = ok && encode_map_4d(&tv, vcache, {U64(D), P, H, n}, {row, row * P, row * P * H}, {64, box, 1, 1},
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-  ok = ok && (g.k_group_major ? encode_map_4d(&tk, kcache, {16, P, H * G, n}, {32, 32 * P, row * P * H}, {16, box, 1, 1},
-                                              CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B)
-                              : encode_map_4d(&tk, kcache, {U64(D), P, H, n}, {row, row * P, row * P * H}, {64, box, 1, 1},
-                                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B));
+  const cuuint64_t P = g.page_size, H = H_kv, n = g.n_pages, G = D / 16, C = D / 64, row = 2 * D;
+  const cuuint32_t box = a.box_rows;
+  TreeMaps tm;
+  const cuuint64_t dq[4] = {cuuint64_t(D), cuuint64_t(H_q), cuuint64_t(T), cuuint64_t(B)}, sq[3] = {row, row * H_q, row * H_q * T};
+  const cuuint32_t bq[4] = {16, cuuint32_t(R), cuuint32_t(a.tile_nodes), 1};
+  const cuuint64_t dr[5] = {64, P, C, H, n}, sr[4] = {row, 128, row * P, row * P * H};
+  const cuuint64_t dg[5] = {16, P, G, H, n}, sg[4] = {32, 32 * P, row * P, row * P * H};
+  const cuuint32_t bv[5] = {64, box, cuuint32_t(C), 1, 1};
+  bool ok = encode_map(&tm.q, q, 4, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
+            encode_map(&tm.v, vcache, 5, dr, sr, bv, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  for (int w = 0; ok && w < 3; ++w) {
+    // boxes of several groups only where one box holds a whole sub-tile
+    const cuuint32_t wide = box == 64 ? 1u << w : 1u;
+    const cuuint32_t bg[5] = {16, box, wide, 1, 1}, br[5] = {64, box, wide < C ? wide : cuuint32_t(C), 1, 1};
+    ok = g.k_group_major
+             ? encode_map(&tm.k[w], kcache, 5, dg, sg, bg, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B)
+             : encode_map(&tm.k[w], kcache, 5, dr, sr, br, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+  }
   if (!ok) return WP_ERR_CUDA;
-  return from_cuda(launch_tree(tq, tk, tv, a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_tree(tm, a, static_cast<cudaStream_t>(stream)));
 }
 
 int wp_kv_compact(void *kcache, int k_layout, void *vcache, const int32_t *lens, const int32_t *path, int A,

@@ -11,13 +11,16 @@
 // The rows of one KV head are its R = Hq/Hkv query heads of every node, row
 // m = node * R + head: they share every K/V tile. One CTA takes up to 128 rows
 // (whole nodes) and one range of keys, in sub-tiles of 64:
-//   warp 4    TMA producer: Q once; per sub-tile the K pieces that a live
-//             group needs (group-major K: one 16-dim box per group; K in rows:
-//             64-dim boxes, four groups each) and V. A box never crosses a
-//             page: it has gcd(page size, 64) rows.
-//   warp 5    issuer: S = sum of one M128 N64 K16 product per live group, O +=
-//             P V (P bf16 in TMEM, V MN-major). S has two 64-column halves, so
-//             the softmax of u runs beside the products of u + 1.
+//   warps 4-5 TMA producers: Q once, and per sub-tile the K pieces that a live
+//             group needs (group-major K: 16-dim groups; K in rows: 64-dim
+//             chunks of four groups); V. A box never crosses a page: it has
+//             gcd(page size, 64) rows.
+//   warp 6    issuer of S = sum of one M128 N64 K16 product per live group. S
+//             has two 64-column halves, so the softmax of u runs beside the
+//             products of u + 1.
+//   warp 7    issuer of O += P V (P bf16 in S's place, V MN-major). One warp
+//             for both was what bounded the kernel: issuing a sub-tile's 12
+//             products and their commits took it about 1800 cycles.
 //   warps 0-3 softmax, a row per thread, online in base 2; O is rescaled only
 //             when a maximum grows by more than 2^8.
 // Groups whose cutoff falls inside a sub-tile's distances go first, one cutoff
@@ -42,8 +45,8 @@ namespace wp {
 namespace {
 
 constexpr int SUB = 64;  // keys per sub-tile
-constexpr int NTHREADS = 192;
-constexpr int PRODUCER_WARP = 4, MMA_WARP = 5;
+constexpr int NTHREADS = 256;
+constexpr int K_WARP = 4, V_WARP = 5, QK_WARP = 6, PV_WARP = 7;
 constexpr int SMEM_PER_CTA = 115712;  // (228 KB - 2 x 1 KB reserved) / 2
 constexpr uint32_t TMEM_COLS = 256;  // two CTAs per SM share 512
 constexpr uint32_t COL_S = 0, COL_O = 128;
@@ -54,7 +57,7 @@ constexpr uint32_t CHUNK = SUB * 128;  // 64 keys x 64 bf16 (V, and K in rows)
 // rows rounded up to 8), then the nodes and barriers. The products read 128
 // rows from each Q tile: what lies beyond a tile's rows (the next tile, or the
 // space behind the last) only makes rows of S and O that nobody reads.
-constexpr uint32_t NUM_BARS = 1 + 4 * TREE_MAX_STAGES + 2 + 2 + 5;
+constexpr uint32_t NUM_BARS = 1 + 4 * TREE_MAX_STAGES + 3 * 2 + 5;
 
 template <int D>
 struct Layout {
@@ -83,6 +86,28 @@ struct Ring {
     }
   }
 };
+
+// 5-D tiled TMA load into this CTA's shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Where the boxes of a sub-tile lie: lane i looks up box i % boxes, one
+// sub-tile ahead of its loads (a block table's entry arrives meanwhile).
+struct Place {
+  int page, row;  // page < 0: behind the last key, nothing to load
+};
+__device__ __forceinline__ Place place_of(const CacheGeom &g, int b, int key, int end) {
+  if (key >= end) return Place{-1, 0};
+  if (g.block_table == nullptr) return Place{b, key};
+  const int j = key / g.page_size;
+  return Place{g.block_table[static_cast<int64_t>(b) * g.max_pages + j], key - j * g.page_size};
+}
 
 struct Plan {
   int len, n, total, tiles;  // context keys, nodes, keys, sub-tiles
@@ -138,8 +163,7 @@ __device__ __forceinline__ void keep_columns(uint32_t (&su)[64], uint64_t bits, 
 
 template <int D, bool KGM>
 __global__ void __launch_bounds__(NTHREADS, 2)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a) {
+    tree_kernel(const __grid_constant__ TreeMaps tm, const __grid_constant__ TreeArgs a) {
   constexpr int G = D / 16;
   constexpr uint32_t STAGE = Layout<D>::STAGE;
   constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, SUB, false, false);
@@ -153,7 +177,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   int32_t *jump = depth + 64;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L.bar_off);
   uint64_t *q_full = bars, *k_full = q_full + 1, *k_empty = k_full + TREE_MAX_STAGES, *v_full = k_empty + TREE_MAX_STAGES,
-           *v_empty = v_full + TREE_MAX_STAGES, *s_ready = v_empty + TREE_MAX_STAGES, *p_ready = s_ready + 2, *o_ready = p_ready + 2, *o_final = o_ready + 1,
+           *v_empty = v_full + TREE_MAX_STAGES, *s_ready = v_empty + TREE_MAX_STAGES, *p_ready = s_ready + 2, *o_ready = p_ready + 2, *o_final = o_ready + 2,
            *bnd_ready = o_final + 1, *bnd_done = bnd_ready + 1, *drain = bnd_done + 1;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L.misc_off);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L.misc_off + 4);
@@ -190,22 +214,23 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_ready[s], 1);
       mbar_init(&p_ready[s], warps);
+      mbar_init(&o_ready[s], 1);
     }
-    mbar_init(o_ready, 1);
     mbar_init(o_final, 1);
     mbar_init(bnd_ready, 1);
     mbar_init(bnd_done, warps);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     fence_barrier_init();
   }
-  if (warp == MMA_WARP) {
+  if (warp == QK_WARP) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
   // The nodes: what each one sees (itself and its ancestors) and its depth, by
   // pointer doubling: after step i a node has joined 2^i of its ancestors.
   bool bad = !plan.ok;
-  if (warp == PRODUCER_WARP) {
+  if (warp == K_WARP) {
     int j[2];
     uint64_t m[2];
 #pragma unroll
@@ -250,7 +275,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     if (lane == 0) *s_deepest = deep;
   } else if (!bad && cg.block_table != nullptr) {
     // a page outside the pool spoils this CTA's rows (its loads would return zeros)
-    const int other = threadIdx.x < PRODUCER_WARP * 32 ? threadIdx.x : threadIdx.x - 32;
+    const int other = threadIdx.x < K_WARP * 32 ? threadIdx.x : threadIdx.x - 32;
     if (k_begin < k_end)
       for (int64_t j = k_begin / cg.page_size + other; j <= (k_end - 1) / cg.page_size; j += NTHREADS - 32)
         bad = bad || cache_page(cg, b, static_cast<int>(j * cg.page_size)) < 0;
@@ -262,119 +287,103 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   const int deepest = *s_deepest;
   // The rows' place among the 128 lanes. A warp reaches the lanes of its own
   // quarter only, and warps w of both CTAs of an SM share a scheduler: few rows
-  // go to other quarters in the CTA that got the upper half of TMEM, and one
-  // warp of rows also stays off the schedulers of the producer and the issuer.
+  // go to other quarters in the CTA that got the upper half of TMEM, one warp of
+  // rows to the quarters whose schedulers the producers' warps share, not the
+  // issuers'.
   const int half = (tmem & 0xffffu) >= TMEM_COLS ? 1 : 0;
-  const int warp0 = warps == 1 ? 2 + half : warps == 2 ? 2 * half : 0;
+  const int warp0 = warps == 1 ? half : warps == 2 ? 2 * half : 0;
   const int nsub = bad ? 0 : nsub_all;
   const int my_cut = lane < G ? a.cut[lane] : 0;
 
-  if (warp == PRODUCER_WARP) {
-    // ------------------------------------------------------------ producer
-    // Lane i looks up where box i % boxes of a sub-tile lies, one sub-tile
-    // ahead of its loads (the block table's entry arrives meanwhile); one
-    // elected lane issues every copy, in a warp-uniform loop.
+  const int box = a.box_rows, boxes = SUB / box;
+  const int first_key = k_begin + (lane & (boxes - 1)) * box;  // this lane's box of sub-tile 0
+
+  if (warp == K_WARP) {
+    // ---------------------------------------------------- producer of Q, K
+    // One elected lane issues every copy, in a warp-uniform loop. A run of
+    // live groups goes in boxes of 4, 2 and 1 groups where a sub-tile is one
+    // box high (an issue costs about 100 cycles, whatever its size).
     const bool leader = elect_one();
-    const int box = a.box_rows, boxes = SUB / box;
-    Ring kr, vr;  // of the next K and V load; a slot is free once its previous round was consumed
-    int k_issued = 0, v_issued = 0;
-    bool ok = true;
-    struct Place {
-      int page, row;  // page < 0: behind the last key, nothing to load
-    };
-    const auto place_of = [&](int u) -> Place {
-      const int key = k_begin + u * SUB + (lane & (boxes - 1)) * box;
-      Place p{-1, 0};
-      if (u < nsub && key < plan.total) {
-        if (cg.block_table == nullptr) {
-          p = Place{b, key};
-        } else {
-          const int j = key / cg.page_size;
-          p = Place{cg.block_table[static_cast<int64_t>(b) * cg.max_pages + j], key - j * cg.page_size};
-        }
-      }
-      return p;
-    };
+    Ring ring;  // of the next load; a slot is free once its previous round was consumed
+    int issued = 0;
     if (nsub > 0 && leader) {
       mbar_arrive_expect_tx(q_full, G * 32u * R * a.tile_nodes);
       for (int g = 0; g < G; ++g)
-        tma_load_4d(smem + L.q_off + g * L.q_tile, &tm_q, q_full, 16 * g, hk * R, mt * a.tile_nodes, b);
+        tma_load_4d(smem + L.q_off + g * L.q_tile, &tm.q, q_full, 16 * g, hk * R, mt * a.tile_nodes, b);
     }
     __syncwarp();
-    const auto load_v = [&](int u, Place pl) -> bool {
-      const int st = vr.slot;
-      if (u >= VST && !warp_wait_idle(&v_empty[st], vr.round ^ 1u, lim, abort_flag)) return false;
-      const int have = __popc(__ballot_sync(FULL, lane < boxes && pl.page >= 0));
-      if (leader) mbar_arrive_expect_tx(&v_full[st], have * box * D * 2u);
-      uint8_t *dst = smem + L.v_off + st * STAGE;
-      for (int i = 0; i < have; ++i) {  // the boxes that exist come first
-        const int page = __shfl_sync(FULL, pl.page, i), row = __shfl_sync(FULL, pl.row, i);
-        if (leader) {
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(dst + c * CHUNK + i * box * 128, &tm_v, &v_full[st], 64 * c, row, hk, page);
-        }
-        __syncwarp();
-      }
-      ++v_issued;
-      vr.next(VST);
-      return true;
-    };
-    Place here = place_of(0), before = here;
-    for (int u = 0; ok && u < nsub; ++u) {
-      const Place next = place_of(u + 1);
-      const int st = kr.slot;
+    Place here = place_of(cg, b, first_key, k_end);
+    for (int u = 0; u < nsub; ++u) {
+      const Place next = place_of(cg, b, first_key + (u + 1) * SUB, k_end);
+      uint64_t *full = &k_full[ring.slot];
+      uint8_t *dst = smem + ring.slot * STAGE;
       const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
       uint32_t need = (cls | (cls >> 8)) & 0xffu;
       if (!KGM) need = ((need & 0xfu) ? 1u : 0u) | ((need >> 4) ? 2u : 0u);  // 64-dim chunks
-      if (u >= KST && !warp_wait_idle(&k_empty[st], kr.round ^ 1u, lim, abort_flag)) {
-        ok = false;
-        break;
-      }
+      if (u >= KST && !warp_wait_idle(&k_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) break;
       const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
-      if (leader) mbar_arrive_expect_tx(&k_full[st], have * __popc(need) * box * (KGM ? 32u : 128u));
-      uint8_t *dst = smem + st * STAGE;
-      for (int i = 0; i < have; ++i) {
+      if (leader) mbar_arrive_expect_tx(full, have * __popc(need) * box * (KGM ? 32u : 128u));
+      for (int i = 0; i < have; ++i) {  // the boxes that exist come first
         const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
         if (leader) {
-#pragma unroll
-          for (int g = 0; g < (KGM ? G : D / 64); ++g)
-            if ((need >> g) & 1u) {
-              if (KGM)
-                tma_load_4d(dst + g * K_TILE + i * box * 32, &tm_k, &k_full[st], 0, row, hk * G + g, page);
-              else
-                tma_load_4d(dst + g * CHUNK + i * box * 128, &tm_k, &k_full[st], 64 * g, row, hk, page);
-            }
+          uint32_t left = need;
+          while (left) {
+            const int g = __ffs(left) - 1;
+            const uint32_t run = left >> g;
+            const int w = boxes > 1 ? 0 : KGM && (run & 0xfu) == 0xfu ? 2 : (run & 3u) == 3u ? 1 : 0;  // log2 of the box
+            if (KGM)
+              tma_load_5d(dst + g * K_TILE + i * box * 32, &tm.k[w], full, 0, row, g, hk, page);
+            else
+              tma_load_5d(dst + g * CHUNK + i * box * 128, &tm.k[w], full, 0, row, g, hk, page);
+            left &= ~(((1u << (1 << w)) - 1) << g);
+          }
         }
         __syncwarp();
       }
-      ++k_issued;
-      kr.next(KST);
-      if (u >= 1) ok = load_v(u - 1, before);
-      before = here;
+      ++issued;
+      ring.next(KST);
       here = next;
     }
-    if (ok && nsub > 0) ok = load_v(nsub - 1, before);
     // no bulk copy may still be in flight when this CTA's shared memory goes
     if (nsub > 0) warp_wait_idle(q_full, 0, lim, nullptr);
-    for (int s = 0; s < KST && s < k_issued; ++s) {
-      const int last = s + ((k_issued - 1 - s) / KST) * KST;
+    for (int s = 0; s < KST && s < issued; ++s) {
+      const int last = s + ((issued - 1 - s) / KST) * KST;
       warp_wait_idle(&k_full[s], (last / KST) & 1, lim, nullptr);
     }
-    for (int s = 0; s < VST && s < v_issued; ++s) {
-      const int last = s + ((v_issued - 1 - s) / VST) * VST;
+  } else if (warp == V_WARP) {
+    // ------------------------------------------------------- producer of V
+    const bool leader = elect_one();
+    Ring ring;
+    int issued = 0;
+    Place here = place_of(cg, b, first_key, k_end);
+    for (int u = 0; u < nsub; ++u) {
+      const Place next = place_of(cg, b, first_key + (u + 1) * SUB, k_end);
+      uint64_t *full = &v_full[ring.slot];
+      if (u >= VST && !warp_wait_idle(&v_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) break;
+      const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
+      if (leader) mbar_arrive_expect_tx(full, have * box * D * 2u);
+      for (int i = 0; i < have; ++i) {
+        const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
+        if (leader) tma_load_5d(smem + L.v_off + ring.slot * STAGE + i * box * D * 2, &tm.v, full, 0, row, 0, hk, page);
+        __syncwarp();
+      }
+      ++issued;
+      ring.next(VST);
+      here = next;
+    }
+    for (int s = 0; s < VST && s < issued; ++s) {
+      const int last = s + ((issued - 1 - s) / VST) * VST;
       warp_wait_idle(&v_full[s], (last / VST) & 1, lim, nullptr);
     }
-  } else if (warp == MMA_WARP) {
-    // -------------------------------------------------------------- issuer
+  } else if (warp == QK_WARP) {
+    // --------------------------------------------------------- issuer of S
+    // S(u) into half u & 1, once P V(u - 2) has read the P that lies there.
     const bool leader = elect_one();
     // row 0 of Q stands in lane 32 * warp0: the tile begins that many rows earlier
     const uint64_t q_desc = smem_desc(smem_u32(smem + L.q_off) - warp0 * 1024, 16, 256, SMEM_SWIZZLE_32B);
     const uint64_t k_desc = KGM ? smem_desc(smem_u32(smem), 16, 256, SMEM_SWIZZLE_32B)
                                 : smem_desc(smem_u32(smem), 16, 1024, SMEM_SWIZZLE_128B);
-    // V: dims contiguous (MN-major); 8-key row groups 1024 B, 64-dim chunks CHUNK apart
-    const uint64_t v_desc = smem_desc(smem_u32(smem + L.v_off), CHUNK, 1024, SMEM_SWIZZLE_128B);
-    Ring kr, vr;  // of the next S and P V products
+    Ring ring;
     int bnd_cnt = 0;
     bool ok = nsub > 0 && warp_wait(q_full, 0, lim, abort_flag);
     const auto issue_groups = [&](uint32_t s_col, uint64_t kst_desc, uint32_t groups, uint32_t acc) {
@@ -387,77 +396,78 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           acc = 1;
         }
     };
-    const auto issue_qk = [&](int u) -> bool {
-      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
+    for (int u = 0; ok && u < nsub; ++u) {
       const int hh = u & 1;
+      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
       const uint32_t s_col = tmem + COL_S + SUB * hh;
-      const uint64_t kst_desc = k_desc + ((kr.slot * STAGE) >> 4);
+      const uint64_t kst_desc = k_desc + ((ring.slot * STAGE) >> 4);
+      ok = warp_wait(&k_full[ring.slot], ring.round, lim, abort_flag) &&
+           (u < 2 || warp_wait(&o_ready[hh], ((u >> 1) - 1) & 1, lim, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
       uint32_t acc = 0;
       const uint32_t bnd = cls >> 8;
       if (bnd) {
+        // boundary classes first, ascending cutoff; each one masked in place
         int64_t prev = -1;
         int32_t W;
         uint32_t groups;
-        while (next_boundary_class(a.cut, bnd, prev, &W, &groups)) {
+        while (ok && next_boundary_class(a.cut, bnd, prev, &W, &groups)) {
           if (leader) {
             issue_groups(s_col, kst_desc, groups, acc);
             umma_commit(bnd_ready);
           }
           acc = 1;
           __syncwarp();
-          if (!warp_wait(bnd_done, bnd_cnt & 1, lim, abort_flag)) return false;
+          ok = warp_wait(bnd_done, bnd_cnt & 1, lim, abort_flag);
           tc_fence_after();
           ++bnd_cnt;
           prev = W;
         }
+        if (!ok) break;
       }
       if (leader) {
         issue_groups(s_col, kst_desc, cls & 0xffu, acc);
         umma_commit(&s_ready[hh]);
-        umma_commit(&k_empty[kr.slot]);
+        umma_commit(&k_empty[ring.slot]);
       }
       __syncwarp();
-      kr.next(KST);
-      return true;
-    };
-    for (int u = 0; ok && u < min(2, nsub); ++u) {
-      ok = warp_wait(&k_full[kr.slot], kr.round, lim, abort_flag);
-      if (ok) {
-        tc_fence_after();
-        ok = issue_qk(u);
-      }
+      ring.next(KST);
     }
-    for (int u = 0; ok && u < nsub; ++u) {
-      const int hh = u & 1, vst = vr.slot;
-      if (!warp_wait(&v_full[vst], vr.round, lim, abort_flag) || !warp_wait(&p_ready[hh], (u >> 1) & 1, lim, abort_flag)) {
-        ok = false;
+    // every product must have finished before TMEM is given back
+    if (leader) umma_commit(&drain[0]);
+    __syncwarp();
+    warp_wait(&drain[0], 0, lim, nullptr);
+  } else if (warp == PV_WARP) {
+    // --------------------------------------------------------- issuer of O
+    const bool leader = elect_one();
+    // V: dims contiguous (MN-major), one box after the other; in a box 8-key row
+    // groups lie 1024 B apart and 64-dim chunks box * 128 B
+    const uint64_t v_desc = smem_desc(smem_u32(smem + L.v_off), box * 128, 1024, SMEM_SWIZZLE_128B);
+    const uint32_t v_in = (box * 128) >> 4, v_step = box > 16 ? 2048 >> 4 : (D / 64) * v_in;  // 16 keys on
+    const uint32_t v_jump = box == 32 ? ((D / 64) * v_in - (4096 >> 4)) : 0u;               // from box 0 to box 1, beyond 2 steps
+    Ring ring;
+    for (int u = 0; u < nsub; ++u) {
+      const int hh = u & 1;
+      const uint64_t vst_desc = v_desc + ((ring.slot * STAGE) >> 4);
+      if (!warp_wait(&v_full[ring.slot], ring.round, lim, abort_flag) || !warp_wait(&p_ready[hh], (u >> 1) & 1, lim, abort_flag))
         break;
-      }
       tc_fence_after();
-      const uint64_t vst_desc = v_desc + ((vst * STAGE) >> 4);
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < SUB / 16; ++kk)
-          umma_ts(tmem + COL_O, tmem + COL_S + SUB * hh + kk * 8, vst_desc + kk * (2048 >> 4), IDESC_PV,
+          umma_ts(tmem + COL_O, tmem + COL_S + SUB * hh + kk * 8, vst_desc + kk * v_step + (kk >= 2 ? v_jump : 0u), IDESC_PV,
                   (u > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(o_ready);
+        umma_commit(&o_ready[hh]);
+        umma_commit(&v_empty[ring.slot]);
         if (u == nsub - 1) umma_commit(o_final);
-        umma_commit(&v_empty[vst]);
       }
       __syncwarp();
-      vr.next(VST);
-      if (u + 2 < nsub) {
-        ok = warp_wait(&k_full[kr.slot], kr.round, lim, abort_flag);
-        if (ok) {
-          tc_fence_after();
-          ok = issue_qk(u + 2);
-        }
-      }
+      ring.next(VST);
     }
-    // every product must have finished before TMEM is given back
-    if (leader) umma_commit(drain);
+    if (leader) umma_commit(&drain[1]);
     __syncwarp();
-    warp_wait(drain, 0, lim, nullptr);
+    warp_wait(&drain[1], 0, lim, nullptr);
   } else if (warp >= warp0 && warp < warp0 + warps) {
     // ------------------------------------------------------------- softmax
     const int r = (warp - warp0) * 32 + lane;  // row of the tile, in TMEM lane 32 * warp + lane
@@ -530,7 +540,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         const float m_new = fmaxf(m_run, m_half);
         if (u > 0) {
           const float alpha = fast_exp2(m_run - m_new);
-          if (!warp_wait(o_ready, (u - 1) & 1, lim, abort_flag)) {
+          if (!warp_wait(&o_ready[hh ^ 1], ((u - 1) >> 1) & 1, lim, abort_flag)) {
             ok = false;
             break;
           }
@@ -558,8 +568,10 @@ __global__ void __launch_bounds__(NTHREADS, 2)
         uint8_t *v = smem + L.v_off + (u % VST) * STAGE;
         const int first = plan.total - k0;
         for (int e = r; e < (SUB - first) * (D / 8); e += warps * 32) {
-          const int rr = first + e / (D / 8), p = e % (D / 8);  // 16-byte piece p of row rr; the swizzle stays in the row
-          *reinterpret_cast<uint4 *>(v + (p / 8) * CHUNK + rr * 128 + (p % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          // 16-byte piece p of row rr; the swizzle stays within a row's 128 bytes
+          const int rr = first + e / (D / 8), p = e % (D / 8), i = rr / box;
+          *reinterpret_cast<uint4 *>(v + i * box * D * 2 + (p / 8) * box * 128 + (rr - i * box) * 128 + (p % 8) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
@@ -627,7 +639,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == MMA_WARP) {
+  if (warp == QK_WARP) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const 
 }
 
 template <int D, bool KGM>
-cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, TreeArgs a, cudaStream_t stream) {
+cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
   // as many stages as let two CTAs share an SM, one more of K than of V where
   // the number is odd
   const int rows = a.tile_nodes * (a.Hq / a.cache.Hkv);
@@ -690,7 +702,7 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, KGM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.row_tiles * a.nsplit, a.cache.Hkv, a.B);
-  tree_kernel<D, KGM><<<grid, NTHREADS, smem, stream>>>(tq, tk, tv, a);
+  tree_kernel<D, KGM><<<grid, NTHREADS, smem, stream>>>(tm, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.nsplit == 1) return e;
   const int64_t all_rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
@@ -700,11 +712,10 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
 
 }  // namespace
 
-cudaError_t launch_tree(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeArgs &a,
-                        cudaStream_t stream) {
+cudaError_t launch_tree(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
   if (a.cache.D == 128)
-    return a.cache.k_group_major ? launch<128, true>(tq, tk, tv, a, stream) : launch<128, false>(tq, tk, tv, a, stream);
-  return a.cache.k_group_major ? launch<64, true>(tq, tk, tv, a, stream) : launch<64, false>(tq, tk, tv, a, stream);
+    return a.cache.k_group_major ? launch<128, true>(tm, a, stream) : launch<128, false>(tm, a, stream);
+  return a.cache.k_group_major ? launch<64, true>(tm, a, stream) : launch<64, false>(tm, a, stream);
 }
 
 }  // namespace wp
