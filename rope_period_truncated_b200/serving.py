@@ -11,8 +11,8 @@ Calls run on ``stream``, or on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+from array import array
 
 import numpy as np
 import torch
@@ -22,17 +22,11 @@ P, I, L, D, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_doubl
 PAGES_OK, PAGES_SHORT, PAGES_BAD_ARGUMENT = range(3)
 TREE_MAX_NODES = 64
 
-
-class _Rows(ctypes.Structure):
-    _fields_ = [("data", P), ("stride_b", L), ("stride_n", L), ("stride_h", L)]
-
-
-_RP = ctypes.POINTER(_Rows)
-SIGNATURES = {
+SIGNATURES = {  # a wp_rows argument is passed by the address of its four 64-bit words
     "wp_cutoffs_partial": (I, [I, I, D, P, D, D, I, P, P]),
     "wp_rope_scaling": (I, [I, D, D, I, D, D, P, P]),
-    "wp_rope_qk": (I, [_RP, _RP, I, _RP, _RP, I, I, I, I, I, P, I, D, P, D, D, I, I, P]),
-    "wp_rope_append": (I, [_RP, _RP, I, _RP, _RP, I, I, I, I, P, P, P, P, I, P, I, I, P, I, I, I, D, P, D, D, I, P]),
+    "wp_rope_qk": (I, [P, P, I, P, P, I, I, I, I, I, P, I, D, P, D, D, I, I, P]),
+    "wp_rope_append": (I, [P, P, I, P, P, I, I, I, I, P, P, P, P, I, P, I, I, P, I, I, I, D, P, D, D, I, P]),
     "wp_decode_tree_workspace_bytes": (S, [I, I, I, I, I, I]),
     "wp_decode_tree": (I, [P, P, I, P, P, P, P, I, I, P, I, I, I, I, I, I, I, P, F, P, P, P, S, P]),
     "wp_kv_compact": (I, [P, I, P, P, P, I, P, P, I, P, I, I, I, I, I, I, P]),
@@ -41,27 +35,35 @@ SIGNATURES = {
     "wp_pages_copy": (I, [P, I, P, P, I, I, I, I, I, P]),
 }
 
+# These calls last a few microseconds on the device at their smallest, so the
+# marshalling counts: one compound test per tensor (the message is looked for
+# only when it fails), tensor addresses as plain integers, no numpy on the way.
+BF16, I32, F32 = torch.bfloat16, torch.int32, torch.float32
+_lib = None
+
 
 def declare(lib):
     """Result and argument types of this module's C calls."""
+    global _lib
     for name, (res, args) in SIGNATURES.items():
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = res, args
+    _lib = lib
 
 
-def _base():
-    import rope_period_truncated_b200 as base
-    return base
+def _load():
+    if _lib is None:
+        import rope_period_truncated_b200 as base
+        base.load_library()
+    return _lib
 
 
-def _call(name, *args):
-    base = _base()
-    code = getattr(base.load_library(), name)(*args)
-    if code:
-        raise base.WavePruneError(name, code)
+def _fail(name, code):
+    from rope_period_truncated_b200 import WavePruneError
+    raise WavePruneError(name, code)
 
 
-def _tensor(t, name, dtype, ndim, device=None, contiguous=True):
+def _complain(t, name, dtype, ndim, device, contiguous):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -70,76 +72,115 @@ def _tensor(t, name, dtype, ndim, device=None, contiguous=True):
         raise ValueError(f"{name} must have {ndim} dims, got shape {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+
+
+def _device(t, name, dtype, ndim, contiguous=True):
+    """Device index of the call's first tensor, the tensor checked."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or t.dim() != ndim or (
+            contiguous and not t.is_contiguous()):
+        _complain(t, name, dtype, ndim, None, contiguous)
+    return t.get_device()
+
+
+def _check(t, name, dtype, ndim, device, contiguous=True):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or t.get_device() != device or (
+            contiguous and not t.is_contiguous()):
+        _complain(t, name, dtype, ndim, device, contiguous)
+
+
+def _current(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the handle without a Stream object around it, where torch offers that
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current)
+
+
+class _Call:
+    """Device and stream of one call: the given stream, or the current one of
+    the tensors' device. Buffers that the call allocates are marked as used on
+    a stream that is not the current one."""
+    __slots__ = ("device", "stream", "handle", "elsewhere")
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.stream = stream
+        self.handle = _current(device)
+        self.elsewhere = False
+        if stream is not None:
+            if stream.device_index != device:
+                raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
+            self.elsewhere = stream.cuda_stream != self.handle
+            self.handle = stream.cuda_stream
+
+    def own(self, t):
+        if self.elsewhere:
+            t.record_stream(self.stream)
+        return t
+
+    def __call__(self, name, *args):
+        fn = getattr(_load(), name)
+        if torch.cuda.current_device() == self.device:
+            code = fn(*args, self.handle)
+        else:
+            with torch.cuda.device(self.device):
+                code = fn(*args, self.handle)
+        if code:
+            _fail(name, code)
+
+
+def _freqs(scale, n):
+    """(what keeps the values alive, their address)"""
+    if scale is None:
+        return None, None
+    a = array("d", scale.tolist() if hasattr(scale, "tolist") else scale)
+    if len(a) != n:
+        raise ValueError(f"freq_scale must have {n} entries (rot_dim/2)")
+    return a, a.buffer_info()[0]
+
+
+def _cuts(group_cut, n):
+    if group_cut is None:
+        return None, None
+    a = array("i", group_cut.tolist() if hasattr(group_cut, "tolist") else group_cut)
+    if len(a) != n:
+        raise ValueError(f"group_cut must have {n} entries (d/16)")
+    return a, a.buffer_info()[0]
+
+
+def _rows(*tensors):
+    """wp_rows of four [B,N,H,d] or [T,H,d] tensors, dims contiguous (None: all zero): the words, the address of each."""
+    words = []
+    for t in tensors:
+        if t is None:
+            words += (0, 0, 0, 0)
+            continue
+        st = t.stride()
+        if st[-1] != 1 and t.shape[-1] > 1:
+            raise ValueError("the head dims must be contiguous")
+        words += (t.data_ptr(), st[0] if len(st) == 4 else 0, st[-3], st[-2])
+    keep = array("q", words)
+    base = keep.buffer_info()[0]
+    return keep, base, base + 32, base + 64, base + 96
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _On:
-    """The launch's device and stream: the given stream, or the current one of the tensors' device. Buffers that a call
-    allocates are marked as used on a stream that is not the current one."""
-
-    def __init__(self, device, stream):
-        current = torch.cuda.current_stream(device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-        self.stream = current if stream is None else stream
-        self.elsewhere = self.stream != current
-        self.guard = contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.device = device
-
-    @property
-    def handle(self):
-        return self.stream.cuda_stream
-
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.elsewhere:
-            t.record_stream(self.stream)
-        return t
-
-
-def _freqs(scale, n):
-    if scale is None:
-        return None, None
-    a = np.ascontiguousarray(scale, dtype=np.float64)
-    if a.shape != (n,):
-        raise ValueError(f"freq_scale must have {n} entries (rot_dim/2)")
-    return a, a.ctypes.data
-
-
-def _cuts(group_cut, n):
-    if group_cut is None:
-        return None, None
-    a = np.ascontiguousarray(group_cut, dtype=np.int32)
-    if a.shape != (n,):
-        raise ValueError(f"group_cut must have {n} entries (d/16)")
-    return a, a.ctypes.data
-
-
-def _rows(t):
-    """wp_rows of a [B,N,H,d] or [T,H,d] tensor whose dims are contiguous."""
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
-        raise ValueError("the head dims must be contiguous")
-    return _Rows(t.data_ptr(), st[0] if t.dim() == 4 else 0, st[-3], st[-2])
-
-
 def _cache(kcache, vcache, block_table, device, B=None, Hkv=None, d=None):
     """(k_layout, B, Lmax, max_pages, page_size, n_pages, Hkv, d) of a cache, its shapes checked."""
-    _tensor(vcache, "vcache", torch.bfloat16, 4, device)
-    n, H, rows, dd = vcache.shape
-    if kcache.dim() == 5:
-        _tensor(kcache, "kcache", torch.bfloat16, 5, device)
-        if tuple(kcache.shape) != (n, H, dd // 16, rows, 16):
+    _check(vcache, "vcache", BF16, 4, device)
+    shape = n, H, rows, dd = vcache.shape
+    if isinstance(kcache, torch.Tensor) and kcache.dim() == 5:
+        _check(kcache, "kcache", BF16, 5, device)
+        if kcache.shape != (n, H, dd // 16, rows, 16):
             raise ValueError("group-major K cache shape mismatch")
         layout = 1
     else:
-        _tensor(kcache, "kcache", torch.bfloat16, 4, device)
-        if kcache.shape != vcache.shape:
+        _check(kcache, "kcache", BF16, 4, device)
+        if kcache.shape != shape:
             raise ValueError("K cache shape mismatch")
         layout = 0
     if (Hkv is not None and H != Hkv) or (d is not None and dd != d):
@@ -148,10 +189,11 @@ def _cache(kcache, vcache, block_table, device, B=None, Hkv=None, d=None):
         if B is not None and n != B:
             raise ValueError(f"the cache holds {n} sequences, expected {B}")
         return layout, n, rows, 0, 0, 0, H, dd
-    _tensor(block_table, "block_table", torch.int32, 2, device)
-    if B is not None and block_table.shape[0] != B:
-        raise ValueError(f"the block table has {block_table.shape[0]} rows, expected {B}")
-    return layout, block_table.shape[0], 0, block_table.shape[1], rows, n, H, dd
+    _check(block_table, "block_table", I32, 2, device)
+    b, pages = block_table.shape
+    if B is not None and b != B:
+        raise ValueError(f"the block table has {b} rows, expected {B}")
+    return layout, b, 0, pages, rows, n, H, dd
 
 
 # --------------------------------------------------------------------- host
@@ -159,10 +201,12 @@ def _cache(kcache, vcache, block_table, device, B=None, Hkv=None, d=None):
 def wp_cutoffs_partial(d_h: int, rot_dim: int, theta: float, layout: int, alpha: float = 2.0, freq_scale=None,
                        scale_all: float = 1.0):
     """Integer cutoffs (chan_cut [rot_dim/2], group_cut [d_h/16]) of a model that rotates the first rot_dim dims."""
-    fs, fs_p = _freqs(freq_scale, rot_dim // 2)
+    keep, fs = _freqs(freq_scale, rot_dim // 2)
     wc = np.zeros(max(rot_dim // 2, 1), dtype=np.int32)
     wg = np.zeros(max(d_h // 16, 1), dtype=np.int32)
-    _call("wp_cutoffs_partial", d_h, rot_dim, theta, fs_p, scale_all, alpha, layout, wc.ctypes.data, wg.ctypes.data)
+    code = _load().wp_cutoffs_partial(d_h, rot_dim, theta, fs, scale_all, alpha, layout, wc.ctypes.data, wg.ctypes.data)
+    if code:
+        _fail("wp_cutoffs_partial", code)
     return wc, wg
 
 
@@ -171,8 +215,10 @@ def wp_rope_scaling(rot_dim: int, theta: float, factor: float, original_len: int
     """(freq_scale [rot_dim/2] float64, amplitude) for a context ``factor`` times ``original_len``."""
     fs = np.zeros(max(rot_dim // 2, 1), dtype=np.float64)
     amp = D(0.0)
-    _call("wp_rope_scaling", rot_dim, theta, factor, original_len, turns_slow, turns_fast, fs.ctypes.data,
-          ctypes.addressof(amp))
+    code = _load().wp_rope_scaling(rot_dim, theta, factor, original_len, turns_slow, turns_fast, fs.ctypes.data,
+                                   ctypes.addressof(amp))
+    if code:
+        _fail("wp_rope_scaling", code)
     return fs, amp.value
 
 
@@ -192,43 +238,49 @@ def wp_rope_qk(q: torch.Tensor | None, k: torch.Tensor | None, theta: float, lay
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
-    _tensor(x, "q" if q is not None else "k", torch.bfloat16, 4, None, False)
-    device = x.device
-    B, N, _, d = x.shape
+    device = _device(x, "q" if q is not None else "k", BF16, 4, False)
+    B, N, H, d = x.shape
+    call = _Call(device, stream)
+    Hq = Hk = 0
+    if q is not None:
+        Hq = H
+        if out_q is None:
+            out_q = torch.empty_like(q)
+            if call.elsewhere:
+                call.own(out_q)
+        else:
+            _check(out_q, "out_q", BF16, 4, device, False)
+            if out_q.shape != q.shape:
+                raise ValueError("out_q shape mismatch")
+    elif out_q is not None:
+        raise ValueError("out_q without q")
     if k is not None:
-        _tensor(k, "k", torch.bfloat16, 4, device, False)
-        if (k.shape[0], k.shape[1], k.shape[3]) != (B, N, d):
+        _check(k, "k", BF16, 4, device, False)
+        ks = k.shape
+        Hk = ks[2]
+        if ks[0] != B or ks[1] != N or ks[3] != d:
             raise ValueError("q/k shape mismatch")
+        if out_k is None:
+            out_k = torch.empty_like(k)
+            if call.elsewhere:
+                call.own(out_k)
+        else:
+            _check(out_k, "out_k", BF16, 4, device, False)
+            if out_k.shape != ks:
+                raise ValueError("out_k shape mismatch")
+    elif out_k is not None:
+        raise ValueError("out_k without k")
     if pos is not None:
-        _tensor(pos, "pos", torch.int32, 2, device)
-        if tuple(pos.shape) != (B, N):
+        _check(pos, "pos", I32, 2, device)
+        if pos.shape != (B, N):
             raise ValueError("pos must be [B, N]")
     rot = d if rot_dim is None else int(rot_dim)
-    on = _On(device, stream)
-    args = []
-    outs = []
-    for t, out, name in ((q, out_q, "out_q"), (k, out_k, "out_k")):
-        if t is None:
-            if out is not None:
-                raise ValueError(f"{name} without its input")
-            args += [None, None, 0]
-            outs.append(None)
-            continue
-        if out is None:
-            out = on.empty(t.shape, torch.bfloat16)
-        else:
-            _tensor(out, name, torch.bfloat16, 4, device, False)
-            if out.shape != t.shape:
-                raise ValueError(f"{name} shape mismatch")
-        args += [_rows(t), _rows(out), t.shape[2]]
-        outs.append(out)
-    if x.numel() == 0:
-        raise ValueError("empty tensors")
-    fs, fs_p = _freqs(freq_scale, rot // 2)
-    with on.guard:
-        _call("wp_rope_qk", *args, B, N, d, rot, _ptr(pos), int(pos0), theta, fs_p, scale_all, amplitude, int(layout),
-              1 if inverse else 0, on.handle)
-    return outs[0], outs[1]
+    keep_f, fs = _freqs(freq_scale, rot // 2)
+    keep, pq, pqo, pk, pko = _rows(q, out_q, k, out_k)
+    call("wp_rope_qk", pq, pqo, Hq, pk, pko, Hk, B, N, d, rot, _ptr(pos), int(pos0), theta, fs, scale_all, amplitude, int(layout),
+         1 if inverse else 0)
+    return out_q, out_k
+
 
 
 def wp_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor,
@@ -238,44 +290,46 @@ def wp_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, kca
     """Rotate the new tokens' q [T,Hq,d] (or None) and k [T,Hkv,d] by pos [T]
     and write k and v [T,Hkv,d] into key slot[i] of sequence seq[i] of the
     cache (int32 [T], device; seq -1 = padding). Returns the rotated q."""
-    _tensor(k, "k", torch.bfloat16, 3, None, False)
-    device = k.device
-    T, Hkv, d = k.shape
-    _tensor(v, "v", torch.bfloat16, 3, device, False)
-    if v.shape != k.shape:
+    device = _device(k, "k", BF16, 3, False)
+    T, Hkv, d = shape = k.shape
+    _check(v, "v", BF16, 3, device, False)
+    if v.shape != shape:
         raise ValueError("k/v shape mismatch")
-    for t, name in ((pos, "pos"), (seq, "seq"), (slot, "slot")):
-        _tensor(t, name, torch.int32, 1, device)
-        if t.shape[0] != T:
-            raise ValueError(f"{name} must be [T]")
+    _check(pos, "pos", I32, 1, device)
+    _check(seq, "seq", I32, 1, device)
+    _check(slot, "slot", I32, 1, device)
+    if len(pos) != T or len(seq) != T or len(slot) != T:
+        raise ValueError("pos, seq and slot must be [T]")
     klay, B, Lmax, max_pages, page, n_pages, _, _ = _cache(kcache, vcache, block_table, device, None, Hkv, d)
     rot = d if rot_dim is None else int(rot_dim)
-    on = _On(device, stream)
-    args = [None, None, 0]
+    call = _Call(device, stream)
+    Hq = 0
     if q is not None:
-        _tensor(q, "q", torch.bfloat16, 3, device, False)
-        if (q.shape[0], q.shape[2]) != (T, d):
+        _check(q, "q", BF16, 3, device, False)
+        qs = q.shape
+        Hq = qs[1]
+        if qs[0] != T or qs[2] != d:
             raise ValueError("q shape mismatch")
         if out_q is None:
-            out_q = on.empty(q.shape, torch.bfloat16)
+            out_q = call.own(torch.empty_like(q))
         else:
-            _tensor(out_q, "out_q", torch.bfloat16, 3, device, False)
-            if out_q.shape != q.shape:
+            _check(out_q, "out_q", BF16, 3, device, False)
+            if out_q.shape != qs:
                 raise ValueError("out_q shape mismatch")
-        args = [_rows(q), _rows(out_q), q.shape[1]]
     elif out_q is not None:
         raise ValueError("out_q without q")
-    fs, fs_p = _freqs(freq_scale, rot // 2)
-    with on.guard:
-        _call("wp_rope_append", *args, _rows(k), _rows(v), Hkv, T, d, rot, _ptr(pos), _ptr(seq), _ptr(slot), _ptr(kcache),
-              klay, _ptr(vcache), B, Lmax, _ptr(block_table), max_pages, page, n_pages, theta, fs_p, scale_all, amplitude,
-              int(layout), on.handle)
+    keep_f, fs = _freqs(freq_scale, rot // 2)
+    keep, pq, pqo, pk, pv = _rows(q, out_q, k, v)
+    call("wp_rope_append", pq, pqo, Hq, pk, pv, Hkv, T, d, rot, pos.data_ptr(), seq.data_ptr(), slot.data_ptr(), kcache.data_ptr(),
+         klay, vcache.data_ptr(), B, Lmax, _ptr(block_table), max_pages, page, n_pages, theta, fs, scale_all, amplitude, int(layout))
     return out_q
+
 
 
 def wp_decode_tree_workspace_bytes(B: int, T: int, Hq: int, Hkv: int, d_h: int, Lmax: int) -> int:
     """Scratch bytes of wp_decode_tree; Lmax: capacity per sequence (paged: max_pages * page size)."""
-    return int(_base().load_library().wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d_h, Lmax))
+    return _load().wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d_h, Lmax)
+
 
 
 def wp_decode_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
@@ -288,42 +342,43 @@ def wp_decode_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, 
     (= T), lens int32 [B]; all on the device. ``group_cut``: group cutoffs
     [d/16] or None (dense). Returns (o [B,T,Hq,d] bf16, lse [B,Hq,T] fp32);
     rows t >= n_nodes[b] are 0 and -inf."""
-    _tensor(q, "q", torch.bfloat16, 4)
-    device = q.device
-    B, T, Hq, d = q.shape
-    _tensor(lens, "lens", torch.int32, 1, device)
-    _tensor(parents, "parents", torch.int32, 2, device)
-    if lens.shape[0] != B or tuple(parents.shape) != (B, T):
+    device = _device(q, "q", BF16, 4)
+    B, T, Hq, d = shape = q.shape
+    _check(lens, "lens", I32, 1, device)
+    _check(parents, "parents", I32, 2, device)
+    if len(lens) != B or parents.shape != (B, T):
         raise ValueError("lens must be [B] and parents [B, T]")
     if n_nodes is not None:
-        _tensor(n_nodes, "n_nodes", torch.int32, 1, device)
-        if n_nodes.shape[0] != B:
+        _check(n_nodes, "n_nodes", I32, 1, device)
+        if len(n_nodes) != B:
             raise ValueError("n_nodes must be [B]")
     klay, _, Lmax, max_pages, page, n_pages, Hkv, _ = _cache(kcache, vcache, block_table, device, B, None, d)
-    on = _On(device, stream)
+    call = _Call(device, stream)
     if out is None:
-        out = on.empty(q.shape, torch.bfloat16)
+        out = call.own(torch.empty_like(q))
     else:
-        _tensor(out, "out", torch.bfloat16, 4, device)
-        if out.shape != q.shape:
+        _check(out, "out", BF16, 4, device)
+        if out.shape != shape:
             raise ValueError("out shape mismatch")
     if lse is not None:
-        _tensor(lse, "lse", torch.float32, 3, device)
-        if tuple(lse.shape) != (B, Hq, T):
+        _check(lse, "lse", F32, 3, device)
+        if lse.shape != (B, Hq, T):
             raise ValueError("lse must be [B, Hq, T]")
     elif want_lse:
-        lse = on.empty((B, Hq, T), torch.float32)
+        lse = call.own(q.new_empty((B, Hq, T), dtype=F32))
     if workspace is None:
-        need = wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d, Lmax if block_table is None else max_pages * page)
-        workspace = on.empty(max(need, 1), torch.uint8)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the same device")
-    cut, cut_p = _cuts(group_cut, d // 16)
-    with on.guard:
-        _call("wp_decode_tree", _ptr(q), _ptr(kcache), klay, _ptr(vcache), _ptr(lens), _ptr(parents), _ptr(n_nodes), T, Lmax,
-              _ptr(block_table), max_pages, page, n_pages, B, Hq, Hkv, d, cut_p, softmax_scale, _ptr(out), _ptr(lse),
-              _ptr(workspace), workspace.numel() * workspace.element_size(), on.handle)
+        ws = _load().wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d, Lmax if block_table is None else max_pages * page)
+        workspace = call.own(lens.new_empty(ws // 4))
+    else:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the same device")
+        ws = workspace.numel() * workspace.element_size()
+    keep, cut = _cuts(group_cut, d // 16)
+    call("wp_decode_tree", q.data_ptr(), kcache.data_ptr(), klay, vcache.data_ptr(), lens.data_ptr(), parents.data_ptr(), _ptr(n_nodes), T,
+         Lmax, _ptr(block_table), max_pages, page, n_pages, B, Hq, Hkv, d, cut, softmax_scale, out.data_ptr(), _ptr(lse),
+         workspace.data_ptr(), ws)
     return out, lse
+
 
 
 def wp_kv_compact(kcache: torch.Tensor, vcache: torch.Tensor, lens: torch.Tensor, path: torch.Tensor, n_keep: torch.Tensor,
@@ -332,25 +387,25 @@ def wp_kv_compact(kcache: torch.Tensor, vcache: torch.Tensor, lens: torch.Tensor
     n_keep[b] (int32 [B,A] increasing, int32 [B]; device), in place. Returns
     the new lengths int32 [B] (``out``, which may be lens; -1 where a path,
     length or page is out of range)."""
-    _tensor(lens, "lens", torch.int32, 1)
-    device = lens.device
-    B = lens.shape[0]
-    _tensor(path, "path", torch.int32, 2, device)
-    _tensor(n_keep, "n_keep", torch.int32, 1, device)
-    if path.shape[0] != B or n_keep.shape[0] != B:
+    device = _device(lens, "lens", I32, 1)
+    B = len(lens)
+    _check(path, "path", I32, 2, device)
+    _check(n_keep, "n_keep", I32, 1, device)
+    rows, A = path.shape
+    if rows != B or len(n_keep) != B:
         raise ValueError("path must be [B, A] and n_keep [B]")
     klay, _, Lmax, max_pages, page, n_pages, Hkv, d = _cache(kcache, vcache, block_table, device, B)
-    on = _On(device, stream)
+    call = _Call(device, stream)
     if out is None:
-        out = on.empty((B,), torch.int32)
+        out = call.own(torch.empty_like(lens))
     else:
-        _tensor(out, "out", torch.int32, 1, device)
-        if out.shape[0] != B:
+        _check(out, "out", I32, 1, device)
+        if len(out) != B:
             raise ValueError("out must be [B]")
-    with on.guard:
-        _call("wp_kv_compact", _ptr(kcache), klay, _ptr(vcache), _ptr(lens), _ptr(path), path.shape[1], _ptr(n_keep), _ptr(out),
-              Lmax, _ptr(block_table), max_pages, page, n_pages, B, Hkv, d, on.handle)
+    call("wp_kv_compact", kcache.data_ptr(), klay, vcache.data_ptr(), lens.data_ptr(), path.data_ptr(), A, n_keep.data_ptr(), out.data_ptr(),
+         Lmax, _ptr(block_table), max_pages, page, n_pages, B, Hkv, d)
     return out
+
 
 
 def wp_pages_update(refs: torch.Tensor, block_table: torch.Tensor, lens: torch.Tensor, parent: torch.Tensor,
@@ -362,37 +417,40 @@ def wp_pages_update(refs: torch.Tensor, block_table: torch.Tensor, lens: torch.T
     [B,max_pages], the others [B]. Returns new tensors (refs, block_table,
     lens, copies [B,3], info [4]); info[0] is PAGES_OK, or PAGES_SHORT /
     PAGES_BAD_ARGUMENT with everything as it was."""
-    _tensor(refs, "refs", torch.int32, 1)
-    device = refs.device
-    _tensor(block_table, "block_table", torch.int32, 2, device)
+    device = _device(refs, "refs", I32, 1)
+    _check(block_table, "block_table", I32, 2, device)
     B, max_pages = block_table.shape
     for t, name in ((lens, "lens"), (parent, "parent"), (keep, "keep"), (new_lens, "new_lens")):
-        _tensor(t, name, torch.int32, 1, device)
-        if t.shape[0] != B:
+        _check(t, name, I32, 1, device)
+        if len(t) != B:
             raise ValueError(f"{name} must be [B]")
-    on = _On(device, stream)
-    n = refs.shape[0]
-    out = [on.empty(s, torch.int32) for s in ((n,), (B, max_pages), (B,), (B, 3), (4,))]
+    call = _Call(device, stream)
+    n = len(refs)
+    refs_out, table_out, lens_out = torch.empty_like(refs), torch.empty_like(block_table), torch.empty_like(lens)
+    copies, info = lens.new_empty((B, 3)), lens.new_empty(4)
     if workspace is None:
-        need = int(_base().load_library().wp_pages_update_workspace_bytes(B, n))
-        workspace = on.empty(max(need, 1), torch.uint8)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the same device")
-    with on.guard:
-        _call("wp_pages_update", _ptr(refs), _ptr(block_table), _ptr(lens), _ptr(parent), _ptr(keep), _ptr(new_lens),
-              *(_ptr(t) for t in out), B, max_pages, int(page_size), n, _ptr(workspace),
-              workspace.numel() * workspace.element_size(), on.handle)
-    return tuple(out)
+        ws = _load().wp_pages_update_workspace_bytes(B, n)
+        workspace = call.own(lens.new_empty(ws // 4))
+    else:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the same device")
+        ws = workspace.numel() * workspace.element_size()
+    if call.elsewhere:
+        for t in (refs_out, table_out, lens_out, copies, info):
+            call.own(t)
+    call("wp_pages_update", refs.data_ptr(), block_table.data_ptr(), lens.data_ptr(), parent.data_ptr(), keep.data_ptr(),
+         new_lens.data_ptr(), refs_out.data_ptr(), table_out.data_ptr(), lens_out.data_ptr(), copies.data_ptr(), info.data_ptr(), B,
+         max_pages, int(page_size), n, workspace.data_ptr(), ws)
+    return refs_out, table_out, lens_out, copies, info
+
 
 
 def wp_pages_copy(k_pages: torch.Tensor, v_pages: torch.Tensor, copies: torch.Tensor, stream=None) -> None:
     """Copy rows between pages of a K and a V pool: copies int32 [n,3] (device),
     each source page, target page, rows; entries of -1 copy nothing."""
-    _tensor(copies, "copies", torch.int32, 2)
-    if copies.shape[1] != 3:
+    device = _device(copies, "copies", I32, 2)
+    n, width = copies.shape
+    if width != 3:
         raise ValueError("copies must be [n, 3]")
-    klay, _, _, _, page, n_pages, Hkv, d = _cache(k_pages, v_pages, copies, copies.device)
-    on = _On(copies.device, stream)
-    with on.guard:
-        _call("wp_pages_copy", _ptr(k_pages), klay, _ptr(v_pages), _ptr(copies), copies.shape[0], n_pages, page, Hkv, d,
-              on.handle)
+    klay, _, _, _, page, n_pages, Hkv, d = _cache(k_pages, v_pages, copies, device)
+    _Call(device, stream)("wp_pages_copy", k_pages.data_ptr(), klay, v_pages.data_ptr(), copies.data_ptr(), n, n_pages, page, Hkv, d)
