@@ -27,10 +27,13 @@ namespace cg = cooperative_groups;
 // holder and is never handed out in the same call: its copy reads rows that
 // no other copy writes.
 //
-// One cluster of CLUSTER blocks does it all: the steps are ordered by the
-// hardware's cluster barrier instead of by launches or by waiting on flags.
+// One cluster of up to 8 blocks does it all: its steps are ordered by the
+// hardware's cluster barrier instead of by launches or by waiting on flags. It
+// is a chain of a dozen dependent memory accesses and four barriers, so its
+// time is latency: few steps, and no more blocks than have work.
 constexpr int PG_THREADS = 1024;
-constexpr int CLUSTER = 8;
+constexpr int MAX_CLUSTER = 8;
+constexpr int PER_THREAD = 4;  // pages ranked by a thread at a time
 
 __device__ __forceinline__ int pages_of(int tokens, int P) { return tokens / P + (tokens % P != 0); }
 
@@ -62,24 +65,29 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
   return warp_sums[warp] + inc - x;
 }
 
-__global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
-    pages_update_kernel(const __grid_constant__ PagesArgs a) {
+// Copies of a page with r holders, w of them rows that will write into it.
+__device__ __forceinline__ int copies_of(int r, int w) { return r > 1 ? (w == r ? w - 1 : w) : 0; }
+
+__global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_constant__ PagesArgs a) {
   __shared__ int warp_sums[33];
-  __shared__ int s_bad, s_free;
+  __shared__ int s_bad, s_lost, s_free, s_below;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = static_cast<int>(cluster.block_rank());
+  const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
   const int tid = rank * PG_THREADS + threadIdx.x;
-  constexpr int NT = CLUSTER * PG_THREADS;
+  const int NT = blocks * PG_THREADS;
   const int P = a.page_size, MP = a.max_pages;
   const int64_t cap = static_cast<int64_t>(MP) * P;
-  if (threadIdx.x == 0) s_bad = s_free = 0;
+  const int warp = tid / 32, lane = tid % 32, warps = NT / 32;  // a warp takes a row of the tables
+  if (threadIdx.x == 0) s_bad = s_lost = s_free = s_below = 0;
   __syncthreads();
 
   // 1. The counts to work on, and the rows' arguments.
+#pragma unroll 4
   for (int i = tid; i < a.n_pages; i += NT) {
     const int r = a.refs[i];
     if (r < 0) s_bad = 1;
     a.refs_out[i] = r;
+    a.taken[i] = 0;
     a.writers[i] = 0;
     a.first[i] = INT_MAX;
   }
@@ -94,57 +102,55 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
   }
   cluster.sync();
   bool bad = false;
-  for (int c = 0; c < CLUSTER; ++c) bad = bad || *cluster.map_shared_rank(&s_bad, c) != 0;
-  cluster.sync();  // s_bad is written again below
+  for (int c = 0; c < blocks; ++c) bad = bad || *cluster.map_shared_rank(&s_bad, c) != 0;
 
-  // 2. Drop the rows' pages. A count that would fall below 0 has fewer holders
-  // than there are rows: handing such a page out would give it two owners.
-  const int64_t n = static_cast<int64_t>(a.B) * MP;
+  // 2. Drop the rows' pages and take up the kept ones, in two counts: a count
+  // below 0 after the drops has fewer holders than there are rows, and handing
+  // such a page out would give it two owners.
   if (!bad)
-    for (int64_t e = tid; e < n; e += NT) {
-      const int b = static_cast<int>(e / MP), j = static_cast<int>(e - static_cast<int64_t>(b) * MP);
-      if (j < pages_of(a.lens[b], P)) {
-        const int p = a.table[e];
-        if (p < 0 || p >= a.n_pages || atomicSub(&a.refs_out[p], 1) < 1) s_bad = 1;
+    for (int b = warp; b < a.B; b += warps) {
+      const int k = a.keep[b], held = pages_of(a.lens[b], P), kept = pages_of(k, P);
+      const int32_t *row = a.table + static_cast<int64_t>(b) * MP;
+      const int32_t *from = kept ? a.table + static_cast<int64_t>(a.parent[b]) * MP : row;
+      const int partial = a.new_lens[b] > k && k % P != 0 ? kept - 1 : -1;  // the page that row b will write into
+#pragma unroll 2
+      for (int j = lane; j < max(held, kept); j += 32) {
+        if (j < held) {
+          const int p = row[j];
+          if (p < 0 || p >= a.n_pages)
+            s_lost = 1;
+          else
+            atomicSub(&a.refs_out[p], 1);
+        }
+        if (j < kept) {
+          const int p = from[j];
+          if (p >= 0 && p < a.n_pages) {  // else: flagged where its own row drops it
+            atomicAdd(&a.taken[p], 1);
+            if (j == partial) {
+              atomicAdd(&a.writers[p], 1);
+              atomicMin(&a.first[p], b);
+            }
+          }
+        }
       }
     }
   cluster.sync();
-  for (int c = 0; c < CLUSTER; ++c) bad = bad || *cluster.map_shared_rank(&s_bad, c) != 0;
+  for (int c = 0; c < blocks; ++c) bad = bad || *cluster.map_shared_rank(&s_lost, c) != 0;
 
-  // 3. Take up the kept pages, and count who writes into partly filled ones.
-  if (!bad)
-    for (int64_t e = tid; e < n; e += NT) {
-      const int b = static_cast<int>(e / MP), j = static_cast<int>(e - static_cast<int64_t>(b) * MP);
-      if (j < pages_of(a.keep[b], P)) atomicAdd(&a.refs_out[a.table[static_cast<int64_t>(a.parent[b]) * MP + j]], 1);
-    }
-  // Who writes into which partly filled page.
-  if (!bad)
-    for (int b = tid; b < a.B; b += NT) {
-      const int k = a.keep[b];
-      if (a.new_lens[b] > k && k % P != 0) {
-        const int last = a.table[static_cast<int64_t>(a.parent[b]) * MP + k / P];
-        atomicAdd(&a.writers[last], 1);
-        atomicMin(&a.first[last], b);
-      }
-    }
-  cluster.sync();
-  // Free pages of this block's share of the pool.
-  const int share = (a.n_pages + CLUSTER - 1) / CLUSTER;
+  // 3. Free pages of this block's share of the pool, and what each row needs
+  // (every block forms that sum; block 0 writes it down).
+  const int share = ((a.n_pages + blocks - 1) / blocks + PER_THREAD - 1) / PER_THREAD * PER_THREAD;
   const int p0 = min(rank * share, a.n_pages), p1 = min(p0 + share, a.n_pages);
   int mine = 0;
-  for (int i = p0 + threadIdx.x; i < p1; i += PG_THREADS) mine += a.refs_out[i] == 0;
+#pragma unroll 4
+  for (int i = p0 + threadIdx.x; i < p1; i += PG_THREADS) {
+    const int r = a.refs_out[i];
+    mine += r + a.taken[i] == 0;
+    if (r < 0) s_below = 1;
+  }
   int free_here;
   block_scan(mine, warp_sums, &free_here);
   if (threadIdx.x == 0) s_free = free_here;
-  cluster.sync();
-  int free_before = 0, free_all = 0;
-  for (int c = 0; c < CLUSTER; ++c) {
-    const int f = *cluster.map_shared_rank(&s_free, c);
-    free_before += c < rank ? f : 0;
-    free_all += f;
-  }
-
-  // 4. What each row needs (every block forms the sum; block 0 writes it down).
   int64_t total = 0;
   int n_copies = 0;
   if (!bad)
@@ -155,58 +161,75 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
         const int k = a.keep[b], nl = a.new_lens[b];
         if (nl > k && k % P != 0) {
           const int last = a.table[static_cast<int64_t>(a.parent[b]) * MP + k / P];
-          const int r = a.refs_out[last];
+          const int r = a.refs_out[last] + a.taken[last];
           copy = r > 1 && !(a.writers[last] == r && a.first[last] == b);
         }
         need = pages_of(nl, P) - pages_of(k, P) + copy;
       }
       int sum, copies;
       const int off = block_scan(need, warp_sums, &sum);
-      block_scan(copy, warp_sums, &copies);
-      if (rank == 0 && b < a.B) {
-        a.off[b] = static_cast<int>(min(total + off, static_cast<int64_t>(INT_MAX)));
-        a.copying[b] = copy;
+      if (rank == 0) {
+        block_scan(copy, warp_sums, &copies);
+        n_copies += copies;
+        if (b < a.B) {
+          a.off[b] = static_cast<int>(min(total + off, static_cast<int64_t>(INT_MAX)));
+          a.copying[b] = copy;
+        }
       }
       total += sum;
-      n_copies += copies;
     }
-  const bool refused = bad || total > free_all;
-  // refs_out was read by every block above; the ranking below writes it
   cluster.sync();
+  int free_before = 0, free_all = 0;
+  for (int c = 0; c < blocks; ++c) {
+    const int f = *cluster.map_shared_rank(&s_free, c);
+    free_before += c < rank ? f : 0;
+    free_all += f;
+    bad = bad || *cluster.map_shared_rank(&s_below, c) != 0;
+  }
+  const bool refused = bad || total > free_all;
 
-  // 5. Rank the free pages; the lowest `total` of them are taken.
-  if (!refused) {
+  // 4. The new counts; the lowest `total` free pages are taken, in order.
+  {
     int64_t at = free_before;
-    for (int i0 = p0; i0 < p1 && at < total; i0 += PG_THREADS) {
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      const int f = i < p1 && a.refs_out[i] == 0;
+    for (int i0 = p0; i0 < p1; i0 += PG_THREADS * PER_THREAD) {
+      const int i = i0 + static_cast<int>(threadIdx.x) * PER_THREAD;
+      int r[PER_THREAD], w[PER_THREAD], f = 0;
+#pragma unroll
+      for (int e = 0; e < PER_THREAD; ++e) {
+        const bool in = i + e < p1;
+        r[e] = !in ? 1 : refused ? a.refs[i + e] : a.refs_out[i + e] + a.taken[i + e];
+        w[e] = in && !refused ? a.writers[i + e] : 0;
+        f += r[e] == 0;
+      }
       int sum;
-      const int64_t r = at + block_scan(f, warp_sums, &sum);
-      if (f && r < total) {
-        a.order[r] = i;
-        a.refs_out[i] = 1;
+      int64_t rank_of = at + block_scan(f, warp_sums, &sum);
+#pragma unroll
+      for (int e = 0; e < PER_THREAD; ++e) {
+        if (i + e >= p1) continue;
+        int now = r[e] - copies_of(r[e], w[e]);
+        if (r[e] == 0 && !refused) {
+          if (rank_of < total) {
+            a.order[rank_of] = i + e;
+            now = 1;
+          }
+          ++rank_of;
+        }
+        a.refs_out[i + e] = now;
       }
       at += sum;
     }
   }
-  cluster.sync();
+  cluster.sync();  // also: nobody reads another block's shared memory from here on
 
-  // 6. The new rows.
-  if (refused)
-    for (int i = tid; i < a.n_pages; i += NT) a.refs_out[i] = a.refs[i];
-  for (int64_t e = tid; e < n; e += NT) {
-    const int b = static_cast<int>(e / MP), j = static_cast<int>(e - static_cast<int64_t>(b) * MP);
-    int p = -1;
-    if (refused) {
-      p = a.table[e];
-    } else {
-      const int base = pages_of(a.keep[b], P) - a.copying[b];
-      if (j < base)
-        p = a.table[static_cast<int64_t>(a.parent[b]) * MP + j];
-      else if (j < pages_of(a.new_lens[b], P))
-        p = a.order[a.off[b] + j - base];
-    }
-    a.table_out[e] = p;
+  // 5. The new rows.
+  for (int b = warp; b < a.B; b += warps) {
+    const int64_t at = static_cast<int64_t>(b) * MP;
+    const int kept = pages_of(a.keep[b], P), base = refused ? MP : kept - a.copying[b];
+    const int wanted = refused ? MP : pages_of(a.new_lens[b], P);
+    const int32_t *from = refused || kept == 0 ? a.table + at : a.table + static_cast<int64_t>(a.parent[b]) * MP;
+    const int32_t *fresh = a.order + (refused ? 0 : a.off[b] - base);
+#pragma unroll 2
+    for (int j = lane; j < MP; j += 32) a.table_out[at + j] = j < base ? from[j] : j < wanted ? fresh[j] : -1;
   }
   for (int b = tid; b < a.B; b += NT) {
     int src = -1, dst = -1, rows = 0;
@@ -215,7 +238,6 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
       src = a.table[static_cast<int64_t>(a.parent[b]) * MP + k / P];
       dst = a.order[a.off[b]];
       rows = k % P;
-      atomicSub(&a.refs_out[src], 1);
     }
     a.copies[3 * b] = src;
     a.copies[3 * b + 1] = dst;
@@ -228,7 +250,6 @@ __global__ void __cluster_dims__(CLUSTER, 1, 1) __launch_bounds__(PG_THREADS)
     a.info[2] = bad ? 0 : free_all;
     a.info[3] = refused ? 0 : n_copies;
   }
-  cluster.sync();  // no block leaves while another may still read its shared memory
 }
 
 // -------------------------------------------------------------------- copy
@@ -269,57 +290,68 @@ __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const __grid_c
 // increases, so i <= path[i]: a move never overwrites the source of a later
 // one, and a thread that carries its 16-byte column of the rows in order needs
 // nobody else. One block per sequence; a bad path, length or page moves
-// nothing and gives lens_out = -1.
+// nothing and gives lens_out = -1. A chain of dependent loads (length, path,
+// page, row), 8 rows in flight per thread.
 constexpr int COMPACT_THREADS = 256;
 constexpr int BATCH = 8;
 
 __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const __grid_constant__ CompactArgs a) {
-  __shared__ int64_t s_from[COMPACT_MAX_PATH], s_to[COMPACT_MAX_PATH];  // page * page_size + row
+  // element offsets of head 0, dim 0: of V; of K the same in rows, else apart
+  __shared__ int64_t s_from[COMPACT_MAX_PATH], s_to[COMPACT_MAX_PATH];
+  __shared__ int s_row_from[COMPACT_MAX_PATH], s_row_to[COMPACT_MAX_PATH];
+  __shared__ int s_moves;
   const CacheGeom &g = a.cache;
   const int b = blockIdx.x;
   const int len = a.lens[b], n = a.n_keep[b];
+  if (threadIdx.x == 0) s_moves = 0;
   bool bad = len < 0 || n < 0 || n > a.A;
-  if (!bad)
-    for (int i = threadIdx.x; i < n; i += COMPACT_THREADS) {
-      const int p = a.path[static_cast<int64_t>(b) * a.A + i];
-      const int before = i == 0 ? -1 : a.path[static_cast<int64_t>(b) * a.A + i - 1];
-      const int64_t from = static_cast<int64_t>(len) + p;
-      if (p <= before || from >= cache_capacity(g)) {
-        bad = true;
-        break;
-      }
-      const int to = len + i;
-      const int64_t fp = cache_page(g, b, static_cast<int>(from)), tp = cache_page(g, b, to);
-      if (fp < 0 || tp < 0) {
-        bad = true;
-        break;
-      }
-      s_from[i] = fp * g.page_size + from % g.page_size;
-      s_to[i] = tp * g.page_size + to % g.page_size;
+  int first = INT_MAX;  // rows before it stay where they are
+  for (int i = threadIdx.x; i < a.A; i += COMPACT_THREADS) {
+    const int p = a.path[static_cast<int64_t>(b) * a.A + i];
+    const int before = i == 0 ? -1 : a.path[static_cast<int64_t>(b) * a.A + i - 1];
+    if (bad || i >= n) break;
+    const int64_t from = static_cast<int64_t>(len) + p;
+    if (p <= before || from >= cache_capacity(g)) {
+      bad = true;
+      break;
     }
+    const int to = len + i;
+    const int64_t fp = cache_page(g, b, static_cast<int>(from)), tp = cache_page(g, b, to);
+    if (fp < 0 || tp < 0) {
+      bad = true;
+      break;
+    }
+    if (p != i) first = min(first, i);
+    s_row_from[i] = static_cast<int>(from) % g.page_size;
+    s_row_to[i] = to % g.page_size;
+    s_from[i] = fp * g.Hkv * g.page_size * g.D;
+    s_to[i] = tp * g.Hkv * g.page_size * g.D;
+  }
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) a.lens_out[b] = bad ? -1 : len + n;
   if (bad) return;
+  // the path increases, so path[i] = i up to some i and never again
+  if (first != INT_MAX) atomicMax(&s_moves, n - first);
+  __syncthreads();
+  const int start = n - s_moves;
   const int pieces = g.D / 8;
   const int cols = g.Hkv * pieces * 2;  // K and V
   for (int e = threadIdx.x; e < cols; e += COMPACT_THREADS) {
     const bool is_v = e >= g.Hkv * pieces;
     const int x = is_v ? e - g.Hkv * pieces : e;
     const int h = x / pieces, dim = 8 * (x - h * pieces);
-    __nv_bfloat16 *base = is_v ? g.vc : g.kc;
-    auto at = [&](int64_t pr) {
-      const int64_t page = pr / g.page_size;
-      const int row = static_cast<int>(pr - page * g.page_size);
-      return base + (is_v ? v_offset(g, page, h, row, dim) : k_offset(g, page, h, row, dim));
-    };
-    for (int i0 = 0; i0 < n; i0 += BATCH) {
+    const bool split = !is_v && g.k_group_major;
+    const int64_t col = is_v ? v_offset(g, 0, h, 0, dim) : k_offset(g, 0, h, 0, dim);
+    const int row_step = split ? 16 : g.D;
+    __nv_bfloat16 *base = (is_v ? g.vc : g.kc) + col;
+    for (int i0 = start; i0 < n; i0 += BATCH) {
       uint4 v[BATCH];
 #pragma unroll
       for (int j = 0; j < BATCH; ++j)
-        if (i0 + j < n) v[j] = *reinterpret_cast<const uint4 *>(at(s_from[i0 + j]));
+        if (i0 + j < n) v[j] = *reinterpret_cast<const uint4 *>(base + s_from[i0 + j] + static_cast<int64_t>(s_row_from[i0 + j]) * row_step);
 #pragma unroll
       for (int j = 0; j < BATCH; ++j)
-        if (i0 + j < n && s_from[i0 + j] != s_to[i0 + j]) *reinterpret_cast<uint4 *>(at(s_to[i0 + j])) = v[j];
+        if (i0 + j < n) *reinterpret_cast<uint4 *>(base + s_to[i0 + j] + static_cast<int64_t>(s_row_to[i0 + j]) * row_step) = v[j];
     }
   }
 }
@@ -327,8 +359,21 @@ __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_pages_update(const PagesArgs &a, cudaStream_t stream) {
-  pages_update_kernel<<<CLUSTER, PG_THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  // one block per 4096 pages and table entries, up to the portable cluster size
+  const int64_t work = (a.n_pages + static_cast<int64_t>(a.B) * a.max_pages) / 4096 + 1;
+  int blocks = 1;
+  while (blocks < MAX_CLUSTER && blocks < work) blocks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(PG_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = blocks;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pages_update_kernel, a);
 }
 
 cudaError_t launch_pages_copy(const PagesCopyArgs &a, cudaStream_t stream) {

@@ -364,7 +364,7 @@ int wp_kv_compact(void *kcache, int k_layout, void *vcache, const int32_t *lens,
 
 size_t wp_pages_update_workspace_bytes(int B, int n_pages) {
   if (B <= 0 || n_pages <= 0) return 0;
-  return (static_cast<size_t>(n_pages) * 3 + static_cast<size_t>(B) * 2) * sizeof(int32_t);
+  return (static_cast<size_t>(n_pages) * 4 + static_cast<size_t>(B) * 2) * sizeof(int32_t);
 }
 
 int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32_t *lens, const int32_t *parent,
@@ -397,7 +397,8 @@ int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32
   a.lens_out = lens_out;
   a.copies = copies;
   a.info = info;
-  a.writers = static_cast<int32_t *>(workspace);
+  a.taken = static_cast<int32_t *>(workspace);
+  a.writers = a.taken + n_pages;
   a.first = a.writers + n_pages;
   a.order = a.first + n_pages;
   a.off = a.order + n_pages;
