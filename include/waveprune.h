@@ -620,7 +620,7 @@ size_t wp_pages_update_workspace_bytes(int B, int n_pages);
  * If the free pages do not suffice (WP_PAGES_SHORT) or an entry is out of
  * range (WP_PAGES_BAD_ARGUMENT), nothing changes: the outputs are the inputs
  * and copies is empty. No output overlaps an input, another output or the
- * workspace (4-byte aligned; contents on entry do not matter).
+ * workspace (8-byte aligned; contents on entry do not matter).
  * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED (capacity above 2^30), WP_ERR_CUDA.
  */
 int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32_t *lens, const int32_t *parent,

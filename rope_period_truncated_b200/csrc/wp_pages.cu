@@ -33,7 +33,7 @@ namespace cg = cooperative_groups;
 // time is latency: few steps, and no more blocks than have work.
 constexpr int PG_THREADS = 1024;
 constexpr int MAX_CLUSTER = 8;
-constexpr int PER_THREAD = 4;  // pages ranked by a thread at a time
+constexpr int PER_LANE = 8;  // a warp ranks 32 x 8 pages at a time
 
 __device__ __forceinline__ int pages_of(int tokens, int P) { return tokens / P + (tokens % P != 0); }
 
@@ -65,12 +65,19 @@ __device__ __forceinline__ int block_scan(int x, int *warp_sums, int *total) {
   return warp_sums[warp] + inc - x;
 }
 
+constexpr unsigned long long DROP = 1ull, TAKE = 1ull << 32;
+
+// Holders of a page after drops and takes.
+__device__ __forceinline__ int holders(int refs, unsigned long long counts) {
+  return refs - static_cast<int>(counts & 0xffffffffu) + static_cast<int>(counts >> 32);
+}
+
 // Copies of a page with r holders, w of them rows that will write into it.
 __device__ __forceinline__ int copies_of(int r, int w) { return r > 1 ? (w == r ? w - 1 : w) : 0; }
 
 __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_constant__ PagesArgs a) {
   __shared__ int warp_sums[33];
-  __shared__ int s_bad, s_lost, s_free, s_below;
+  __shared__ int s_bad, s_lost, s_free, s_below, s_copies;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
   const int tid = rank * PG_THREADS + threadIdx.x;
@@ -78,7 +85,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
   const int P = a.page_size, MP = a.max_pages;
   const int64_t cap = static_cast<int64_t>(MP) * P;
   const int warp = tid / 32, lane = tid % 32, warps = NT / 32;  // a warp takes a row of the tables
-  if (threadIdx.x == 0) s_bad = s_lost = s_free = s_below = 0;
+  if (threadIdx.x == 0) s_bad = s_lost = s_free = s_below = s_copies = 0;
   __syncthreads();
 
   // 1. The counts to work on, and the rows' arguments.
@@ -86,8 +93,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
   for (int i = tid; i < a.n_pages; i += NT) {
     const int r = a.refs[i];
     if (r < 0) s_bad = 1;
-    a.refs_out[i] = r;
-    a.taken[i] = 0;
+    a.counts[i] = 0;
     a.writers[i] = 0;
     a.first[i] = INT_MAX;
   }
@@ -100,13 +106,28 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
     }
     if (!ok) s_bad = 1;
   }
+  // Row threadIdx.x for step 3 (every block forms that sum): what it needs is
+  // known now but for the counts.
+  int my_kept = 0, my_wanted = 0, my_last = -1;
+  const auto row_of = [&](int b) {
+    my_kept = my_wanted = 0;
+    my_last = -1;
+    if (b >= a.B) return;
+    const int k = a.keep[b], nl = a.new_lens[b], p = a.parent[b];
+    my_kept = pages_of(k, P);
+    my_wanted = pages_of(nl, P);
+    if (k > 0 && k <= cap && nl > k && k % P != 0 && p >= 0 && p < a.B) my_last = a.table[static_cast<int64_t>(p) * MP + k / P];
+  };
+  row_of(threadIdx.x);
+  // Every block's copy of a variable, one lane per block.
+  const auto of_blocks = [&](int *v) { return lane < blocks ? *cluster.map_shared_rank(v, lane) : 0; };
   cluster.sync();
-  bool bad = false;
-  for (int c = 0; c < blocks; ++c) bad = bad || *cluster.map_shared_rank(&s_bad, c) != 0;
+  bool bad = __any_sync(0xffffffffu, of_blocks(&s_bad));
 
-  // 2. Drop the rows' pages and take up the kept ones, in two counts: a count
-  // below 0 after the drops has fewer holders than there are rows, and handing
-  // such a page out would give it two owners.
+  // 2. Drop the rows' pages and take up the kept ones: drops in the low half of
+  // a page's count, takes in the high half, one atomic for both where a row
+  // goes on with its own page (the scattered atomics bound this step). More
+  // drops than holders: handing such a page out would give it two owners.
   if (!bad)
     for (int b = warp; b < a.B; b += warps) {
       const int k = a.keep[b], held = pages_of(a.lens[b], P), kept = pages_of(k, P);
@@ -115,106 +136,100 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
       const int partial = a.new_lens[b] > k && k % P != 0 ? kept - 1 : -1;  // the page that row b will write into
 #pragma unroll 2
       for (int j = lane; j < max(held, kept); j += 32) {
-        if (j < held) {
-          const int p = row[j];
-          if (p < 0 || p >= a.n_pages)
-            s_lost = 1;
-          else
-            atomicSub(&a.refs_out[p], 1);
-        }
-        if (j < kept) {
-          const int p = from[j];
-          if (p >= 0 && p < a.n_pages) {  // else: flagged where its own row drops it
-            atomicAdd(&a.taken[p], 1);
-            if (j == partial) {
-              atomicAdd(&a.writers[p], 1);
-              atomicMin(&a.first[p], b);
-            }
+        const int p = j < held ? row[j] : -1, q = j < kept ? from[j] : -1;
+        const bool p_ok = p >= 0 && p < a.n_pages, q_ok = q >= 0 && q < a.n_pages;
+        if (j < held && !p_ok) s_lost = 1;  // a parent's bad page is flagged where its own row drops it
+        if (p_ok) atomicAdd(&a.counts[p], p == q ? DROP + TAKE : DROP);
+        if (q_ok) {
+          if (p != q) atomicAdd(&a.counts[q], TAKE);
+          if (j == partial) {
+            atomicAdd(&a.writers[q], 1);
+            atomicMin(&a.first[q], b);
           }
         }
       }
     }
   cluster.sync();
-  for (int c = 0; c < blocks; ++c) bad = bad || *cluster.map_shared_rank(&s_lost, c) != 0;
+  bad = __any_sync(0xffffffffu, of_blocks(&s_lost)) || bad;
 
   // 3. Free pages of this block's share of the pool, and what each row needs
   // (every block forms that sum; block 0 writes it down).
-  const int share = ((a.n_pages + blocks - 1) / blocks + PER_THREAD - 1) / PER_THREAD * PER_THREAD;
+  const int share = (a.n_pages + blocks - 1) / blocks;
   const int p0 = min(rank * share, a.n_pages), p1 = min(p0 + share, a.n_pages);
   int mine = 0;
 #pragma unroll 4
   for (int i = p0 + threadIdx.x; i < p1; i += PG_THREADS) {
-    const int r = a.refs_out[i];
-    mine += r + a.taken[i] == 0;
-    if (r < 0) s_below = 1;
+    const int r = a.refs[i];
+    const unsigned long long c = a.counts[i];
+    mine += holders(r, c) == 0;
+    if ((c & 0xffffffffu) > static_cast<unsigned>(r)) s_below = 1;
   }
-  int free_here;
-  block_scan(mine, warp_sums, &free_here);
-  if (threadIdx.x == 0) s_free = free_here;
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) atomicAdd(&s_free, mine);
   int64_t total = 0;
-  int n_copies = 0;
   if (!bad)
     for (int b0 = 0; b0 < a.B; b0 += PG_THREADS) {
       const int b = b0 + static_cast<int>(threadIdx.x);
-      int need = 0, copy = 0;
-      if (b < a.B) {
-        const int k = a.keep[b], nl = a.new_lens[b];
-        if (nl > k && k % P != 0) {
-          const int last = a.table[static_cast<int64_t>(a.parent[b]) * MP + k / P];
-          const int r = a.refs_out[last] + a.taken[last];
-          copy = r > 1 && !(a.writers[last] == r && a.first[last] == b);
-        }
-        need = pages_of(nl, P) - pages_of(k, P) + copy;
+      if (b0 > 0) row_of(b);
+      int copy = 0;
+      if (my_last >= 0) {
+        const int r = holders(a.refs[my_last], a.counts[my_last]);
+        copy = r > 1 && !(a.writers[my_last] == r && a.first[my_last] == b);
       }
-      int sum, copies;
-      const int off = block_scan(need, warp_sums, &sum);
-      if (rank == 0) {
-        block_scan(copy, warp_sums, &copies);
-        n_copies += copies;
-        if (b < a.B) {
-          a.off[b] = static_cast<int>(min(total + off, static_cast<int64_t>(INT_MAX)));
-          a.copying[b] = copy;
-        }
+      const int copies = __reduce_add_sync(0xffffffffu, copy);
+      if (lane == 0) atomicAdd(&s_copies, copies);
+      int sum;
+      const int off = block_scan(my_wanted - my_kept + copy, warp_sums, &sum);
+      if (rank == 0 && b < a.B) {
+        a.off[b] = static_cast<int>(min(total + off, static_cast<int64_t>(INT_MAX)));
+        a.copying[b] = copy;
       }
       total += sum;
     }
   cluster.sync();
-  int free_before = 0, free_all = 0;
-  for (int c = 0; c < blocks; ++c) {
-    const int f = *cluster.map_shared_rank(&s_free, c);
-    free_before += c < rank ? f : 0;
-    free_all += f;
-    bad = bad || *cluster.map_shared_rank(&s_below, c) != 0;
-  }
+  const int theirs = of_blocks(&s_free);
+  bad = __any_sync(0xffffffffu, of_blocks(&s_below)) || bad;
+  const int free_before = __reduce_add_sync(0xffffffffu, lane < rank ? theirs : 0);
+  const int free_all = __reduce_add_sync(0xffffffffu, theirs);
   const bool refused = bad || total > free_all;
 
   // 4. The new counts; the lowest `total` free pages are taken, in order.
   {
     int64_t at = free_before;
-    for (int i0 = p0; i0 < p1; i0 += PG_THREADS * PER_THREAD) {
-      const int i = i0 + static_cast<int>(threadIdx.x) * PER_THREAD;
-      int r[PER_THREAD], w[PER_THREAD], f = 0;
+    constexpr int STEP = PG_THREADS * PER_LANE;
+    for (int i0 = p0; i0 < p1; i0 += STEP) {
+      const int first = i0 + (threadIdx.x / 32) * 32 * PER_LANE + lane;  // this lane's pages: first + 32 e
+      int r[PER_LANE], w[PER_LANE];
+      unsigned free_lanes[PER_LANE];
 #pragma unroll
-      for (int e = 0; e < PER_THREAD; ++e) {
-        const bool in = i + e < p1;
-        r[e] = !in ? 1 : refused ? a.refs[i + e] : a.refs_out[i + e] + a.taken[i + e];
-        w[e] = in && !refused ? a.writers[i + e] : 0;
-        f += r[e] == 0;
+      for (int e = 0; e < PER_LANE; ++e) {
+        const int i = first + 32 * e;
+        const bool in = i < p1;
+        r[e] = !in ? 1 : refused ? a.refs[i] : holders(a.refs[i], a.counts[i]);
+        w[e] = in && !refused ? a.writers[i] : 0;
+      }
+      int f = 0;
+#pragma unroll
+      for (int e = 0; e < PER_LANE; ++e) {
+        free_lanes[e] = __ballot_sync(0xffffffffu, r[e] == 0);
+        f += __popc(free_lanes[e]);
       }
       int sum;
-      int64_t rank_of = at + block_scan(f, warp_sums, &sum);
+      // lane 0 brings the warp's count into the sum; every lane gets what lies before the warp
+      int64_t rank_of = at + __shfl_sync(0xffffffffu, block_scan(lane == 0 ? f : 0, warp_sums, &sum), 0);
 #pragma unroll
-      for (int e = 0; e < PER_THREAD; ++e) {
-        if (i + e >= p1) continue;
-        int now = r[e] - copies_of(r[e], w[e]);
-        if (r[e] == 0 && !refused) {
-          if (rank_of < total) {
-            a.order[rank_of] = i + e;
+      for (int e = 0; e < PER_LANE; ++e) {
+        const int i = first + 32 * e;
+        if (i < p1) {
+          int now = r[e] - copies_of(r[e], w[e]);
+          const int64_t k = rank_of + __popc(free_lanes[e] & ((1u << lane) - 1));
+          if (r[e] == 0 && !refused && k < total) {
+            a.order[k] = i;
             now = 1;
           }
-          ++rank_of;
+          a.refs_out[i] = now;
         }
-        a.refs_out[i + e] = now;
+        rank_of += __popc(free_lanes[e]);
       }
       at += sum;
     }
@@ -248,7 +263,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
     a.info[0] = bad ? WP_PAGES_BAD_ARGUMENT : refused ? WP_PAGES_SHORT : WP_PAGES_OK;
     a.info[1] = bad ? 0 : static_cast<int>(min(total, static_cast<int64_t>(INT_MAX)));
     a.info[2] = bad ? 0 : free_all;
-    a.info[3] = refused ? 0 : n_copies;
+    a.info[3] = refused ? 0 : s_copies;
   }
 }
 

@@ -84,7 +84,8 @@ cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream);
 struct PagesArgs {
   const int32_t *refs, *table, *lens, *parent, *keep, *new_lens;
   int32_t *refs_out, *table_out, *lens_out, *copies, *info;
-  int32_t *taken, *writers, *first, *order;  // scratch [n_pages] each
+  unsigned long long *counts;                // scratch [n_pages]
+  int32_t *writers, *first, *order;          // scratch [n_pages] each
   int32_t *off, *copying;            // scratch [B] each
   int B, max_pages, n_pages, page_size;
 };

@@ -364,7 +364,7 @@ int wp_kv_compact(void *kcache, int k_layout, void *vcache, const int32_t *lens,
 
 size_t wp_pages_update_workspace_bytes(int B, int n_pages) {
   if (B <= 0 || n_pages <= 0) return 0;
-  return (static_cast<size_t>(n_pages) * 4 + static_cast<size_t>(B) * 2) * sizeof(int32_t);
+  return (static_cast<size_t>(n_pages) * 5 + static_cast<size_t>(B) * 2) * sizeof(int32_t);
 }
 
 int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32_t *lens, const int32_t *parent,
@@ -373,7 +373,7 @@ int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32
                     void *workspace, size_t ws_bytes, void *stream) {
   const void *ptrs[] = {refs, block_table, lens, parent, keep, new_lens, refs_out, block_table_out, lens_out, copies, info, workspace};
   for (const void *p : ptrs)
-    if (p == nullptr || !aligned(p, 4)) return WP_ERR_ARG;
+    if (p == nullptr || !aligned(p, p == workspace ? 8 : 4)) return WP_ERR_ARG;
   if (B <= 0 || max_pages <= 0 || page_size < 16 || page_size % 16 != 0 || n_pages <= 0) return WP_ERR_ARG;
   if (static_cast<int64_t>(max_pages) * page_size > (1ll << 30)) return WP_ERR_UNSUPPORTED;
   if (ws_bytes < wp_pages_update_workspace_bytes(B, n_pages)) return WP_ERR_ARG;
@@ -397,8 +397,8 @@ int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32
   a.lens_out = lens_out;
   a.copies = copies;
   a.info = info;
-  a.taken = static_cast<int32_t *>(workspace);
-  a.writers = a.taken + n_pages;
+  a.counts = static_cast<unsigned long long *>(workspace);
+  a.writers = reinterpret_cast<int32_t *>(a.counts + n_pages);
   a.first = a.writers + n_pages;
   a.order = a.first + n_pages;
   a.off = a.order + n_pages;

@@ -186,7 +186,7 @@ def test_pages_update_rejects_bad_arguments(lib):
     good = at[:11] + [B, MP, P, n, at[11], ws, None]
     bad = [({i: None}, ARG, f"pointer {i}") for i in range(11)] + [({i: at[i] + 2}, ARG, f"pointer {i} misaligned") for i in range(11)]
     bad += [({11: 0}, ARG, "B"), ({12: 0}, ARG, "max_pages"), ({13: 8}, ARG, "page size"), ({13: 24}, ARG, "page size"), ({14: 0}, ARG, "pool"),
-            ({15: None}, ARG, "workspace"), ({16: ws - 1}, ARG, "workspace too small"), ({12: 1 << 27}, UNSUPPORTED, "capacity"),
+            ({15: None}, ARG, "workspace"), ({15: at[11] + 4}, ARG, "workspace misaligned"), ({16: ws - 1}, ARG, "workspace too small"), ({12: 1 << 27}, UNSUPPORTED, "capacity"),
             ({6: at[0]}, ARG, "counts in place"), ({7: at[1]}, ARG, "table in place"), ({8: at[2]}, ARG, "lengths in place"),
             ({9: at[7] + 4 * B * MP - 4}, ARG, "copies inside the table"), ({15: at[6]}, ARG, "workspace over an output")]
     _expect(lib.wp_pages_update, good, bad)
