@@ -298,7 +298,7 @@ def wp_rope_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, kca
     _check(pos, "pos", I32, 1, device)
     _check(seq, "seq", I32, 1, device)
     _check(slot, "slot", I32, 1, device)
-    if len(pos) != T or len(seq) != T or len(slot) != T:
+    if pos.shape[0] != T or seq.shape[0] != T or slot.shape[0] != T:
         raise ValueError("pos, seq and slot must be [T]")
     klay, B, Lmax, max_pages, page, n_pages, _, _ = _cache(kcache, vcache, block_table, device, None, Hkv, d)
     rot = d if rot_dim is None else int(rot_dim)
@@ -346,11 +346,11 @@ def wp_decode_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, 
     B, T, Hq, d = shape = q.shape
     _check(lens, "lens", I32, 1, device)
     _check(parents, "parents", I32, 2, device)
-    if len(lens) != B or parents.shape != (B, T):
+    if lens.shape[0] != B or parents.shape != (B, T):
         raise ValueError("lens must be [B] and parents [B, T]")
     if n_nodes is not None:
         _check(n_nodes, "n_nodes", I32, 1, device)
-        if len(n_nodes) != B:
+        if n_nodes.shape[0] != B:
             raise ValueError("n_nodes must be [B]")
     klay, _, Lmax, max_pages, page, n_pages, Hkv, _ = _cache(kcache, vcache, block_table, device, B, None, d)
     call = _Call(device, stream)
@@ -388,11 +388,11 @@ def wp_kv_compact(kcache: torch.Tensor, vcache: torch.Tensor, lens: torch.Tensor
     the new lengths int32 [B] (``out``, which may be lens; -1 where a path,
     length or page is out of range)."""
     device = _device(lens, "lens", I32, 1)
-    B = len(lens)
+    B = lens.shape[0]
     _check(path, "path", I32, 2, device)
     _check(n_keep, "n_keep", I32, 1, device)
     rows, A = path.shape
-    if rows != B or len(n_keep) != B:
+    if rows != B or n_keep.shape[0] != B:
         raise ValueError("path must be [B, A] and n_keep [B]")
     klay, _, Lmax, max_pages, page, n_pages, Hkv, d = _cache(kcache, vcache, block_table, device, B)
     call = _Call(device, stream)
@@ -400,7 +400,7 @@ def wp_kv_compact(kcache: torch.Tensor, vcache: torch.Tensor, lens: torch.Tensor
         out = call.own(torch.empty_like(lens))
     else:
         _check(out, "out", I32, 1, device)
-        if len(out) != B:
+        if out.shape[0] != B:
             raise ValueError("out must be [B]")
     call("wp_kv_compact", kcache.data_ptr(), klay, vcache.data_ptr(), lens.data_ptr(), path.data_ptr(), A, n_keep.data_ptr(), out.data_ptr(),
          Lmax, _ptr(block_table), max_pages, page, n_pages, B, Hkv, d)
@@ -422,10 +422,10 @@ def wp_pages_update(refs: torch.Tensor, block_table: torch.Tensor, lens: torch.T
     B, max_pages = block_table.shape
     for t, name in ((lens, "lens"), (parent, "parent"), (keep, "keep"), (new_lens, "new_lens")):
         _check(t, name, I32, 1, device)
-        if len(t) != B:
+        if t.shape[0] != B:
             raise ValueError(f"{name} must be [B]")
     call = _Call(device, stream)
-    n = len(refs)
+    n = refs.shape[0]
     refs_out, table_out, lens_out = torch.empty_like(refs), torch.empty_like(block_table), torch.empty_like(lens)
     copies, info = lens.new_empty((B, 3)), lens.new_empty(4)
     if workspace is None:
