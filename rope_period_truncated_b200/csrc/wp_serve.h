@@ -107,36 +107,57 @@ struct TreeArgs {
   const int32_t *lens, *parents, *n_nodes;  // [B], [B, T], [B] or null
   __nv_bfloat16 *o;                         // [B, T, Hq, D]
   float *lse;                               // [B, Hq, T] or null
-  float *o_part, *lse_part;                 // [B, Hkv, T * R, nsplit(, D)], lse base 2
+  float *o_part, *lse_part;                 // partial results, lse base 2
+  int64_t *prefix;                          // few rows: [B + 1] key tiles (per head) before each sequence
   int B, T, Hq;
   int tile_nodes, row_tiles;                // nodes per CTA, CTAs per KV head and split
-  int nsplit, box_rows;                     // splits of the keys; rows of one TMA box
+  int nsplit, box_rows;                     // splits of the keys (few rows: CTAs); rows of one TMA box
   int k_stages, v_stages;                   // ring depths, set at the launch
   int32_t cut[8];
   float scale_log2;
   long long wait_limit;
 };
 
-// How the work is cut. Nodes per CTA: as many whole nodes (R rows each) as 128
-// rows hold. Splits: one batch entry fills the 148 SMs x 2 CTAs once, since
-// its splits are equal; several entries have lengths of their own, so their
-// CTAs are cut to fill them about four times over and the SMs even out.
+// How the work is cut. Up to 64 rows per KV head (R query heads of T nodes) go
+// to the kernel whose products have keys and dims as their 128 rows: tiles of
+// 128 keys, one CTA per SM, the tiles of all sequences and KV heads dealt out
+// evenly. More rows go to the one that has query rows there: tiles of whole
+// nodes, 64 keys, two CTAs per SM, each (sequence, KV head) split on its own;
+// one batch entry fills the SMs once, since its splits are equal, several have
+// lengths of their own, so their CTAs are cut to fill them about four times
+// over and the SMs even out.
+constexpr int TREE_FEW_ROWS = 64;
+constexpr int TREE_SMS = 148;
+__host__ __device__ inline bool tree_few_rows(int T, int R) { return T * R <= TREE_FEW_ROWS; }
+inline int tree_key_tile(int T, int R) { return tree_few_rows(T, R) ? 128 : 64; }
 inline int tree_tile_nodes(int T, int R) { return T < 128 / R ? T : 128 / R; }
 inline int tree_splits(int B, int T, int Hkv, int R, int64_t capacity) {
-  const int tile = tree_tile_nodes(T, R), tiles = (T + tile - 1) / tile;
-  const int64_t units = static_cast<int64_t>(B) * Hkv * tiles;
-  const int64_t want = (B == 1 ? 296 : 4 * 296) / units;
+  const int64_t units = static_cast<int64_t>(B) * Hkv;
+  if (tree_few_rows(T, R)) {
+    const int64_t tiles = units * ((capacity + 127) / 128);
+    return static_cast<int>(tiles < TREE_SMS ? tiles : TREE_SMS);
+  }
+  const int tile = tree_tile_nodes(T, R), row_tiles = (T + tile - 1) / tile;
+  const int64_t want = (B == 1 ? 2 * TREE_SMS : 8 * TREE_SMS) / (units * row_tiles);
   const int64_t most = (capacity + 255) / 256;
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n);
 }
-inline size_t tree_partial_o_bytes(int B, int T, int Hq, int nsplit, int D) {
-  return (static_cast<size_t>(B) * T * Hq * nsplit * D * sizeof(float) + 255) & ~static_cast<size_t>(255);
-}
-inline size_t tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int64_t capacity) {
+// The workspace: partial O, partial LSE, prefix sums, each from a multiple of 256.
+struct TreeWorkspace {
+  size_t lse, prefix, bytes;  // offsets, and the whole
+};
+inline TreeWorkspace tree_workspace(int B, int T, int Hq, int Hkv, int D, int64_t capacity) {
   const int nsplit = tree_splits(B, T, Hkv, Hq / Hkv, capacity);
-  if (nsplit == 1) return 256;
-  return tree_partial_o_bytes(B, T, Hq, nsplit, D) + static_cast<size_t>(B) * T * Hq * nsplit * sizeof(float);
+  const bool few = tree_few_rows(T, Hq / Hkv);
+  // few rows: two partial results per CTA, of the rows of one KV head
+  const size_t n = few ? static_cast<size_t>(nsplit) * 2 * T * (Hq / Hkv) : nsplit == 1 ? 0 : static_cast<size_t>(B) * T * Hq * nsplit;
+  const auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  TreeWorkspace w;
+  w.lse = up(n * D * sizeof(float));
+  w.prefix = w.lse + up(n * sizeof(float));
+  w.bytes = w.prefix + up(few ? (static_cast<size_t>(B) + 1) * sizeof(int64_t) : 1);
+  return w;
 }
 
 // Tensor maps. Q: 16 dims of the R heads of tile_nodes nodes. V: box_rows keys
@@ -146,5 +167,6 @@ struct TreeMaps {
   CUtensorMap q, v, k[3];
 };
 cudaError_t launch_tree(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream);
+cudaError_t launch_tree_few(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream);
 
 }  // namespace wp

@@ -275,7 +275,7 @@ int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_row
 size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, int Lmax) {
   if (B <= 0 || T <= 0 || T > TREE_MAX_NODES || H_q <= 0 || H_kv <= 0 || d_h <= 0 || Lmax <= 0) return 0;
   if (H_q % H_kv != 0 || H_q / H_kv > TREE_MAX_GROUP) return 0;
-  return tree_workspace_bytes(B, T, H_q, H_kv, d_h, Lmax);
+  return tree_workspace(B, T, H_q, H_kv, d_h, Lmax).bytes;
 }
 
 int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *vcache, const int32_t *lens,
@@ -313,9 +313,14 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
   a.tile_nodes = tree_tile_nodes(T, R);
   a.row_tiles = (T + a.tile_nodes - 1) / a.tile_nodes;
   a.nsplit = tree_splits(B, T, H_kv, R, cap);
-  a.box_rows = block_table == nullptr || page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
-  a.o_part = static_cast<float *>(workspace);
-  a.lse_part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + tree_partial_o_bytes(B, T, H_q, a.nsplit, D));
+  const int key_tile = tree_key_tile(T, R);
+  a.box_rows = key_tile;  // of one box: never across a page, which holds a multiple of 16 keys
+  while (block_table != nullptr && page_size % a.box_rows != 0) a.box_rows /= 2;
+  const TreeWorkspace w = tree_workspace(B, T, H_q, H_kv, D, cap);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.o_part = reinterpret_cast<float *>(ws);
+  a.lse_part = reinterpret_cast<float *>(ws + w.lse);
+  a.prefix = reinterpret_cast<int64_t *>(ws + w.prefix);
   a.wait_limit = wait_limit();
   const float scale = softmax_scale > 0.f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(double(d_h)));
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
@@ -334,8 +339,8 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
   bool ok = encode_map(&tm.q, q, 4, dq, sq, bq, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) &&
             encode_map(&tm.v, vcache, 5, dr, sr, bv, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
   for (int w = 0; ok && w < 3; ++w) {
-    // boxes of several groups only where one box holds a whole sub-tile
-    const cuuint32_t wide = box == 64 ? 1u << w : 1u;
+    // boxes of several groups only where one box holds a whole tile of keys
+    const cuuint32_t wide = a.box_rows == key_tile ? 1u << w : 1u;
     const cuuint32_t bg[5] = {16, box, wide, 1, 1}, br[5] = {64, box, wide < C ? wide : cuuint32_t(C), 1, 1};
     ok = g.k_group_major
              ? encode_map(&tm.k[w], kcache, 5, dg, sg, bg, CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B)

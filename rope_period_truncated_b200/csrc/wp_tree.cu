@@ -37,16 +37,12 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
-#include "wp_device.cuh"
-#include "wp_prefill_common.cuh"
-#include "wp_serve.h"
+#include "wp_tree.cuh"
 
 namespace wp {
 namespace {
 
 constexpr int SUB = 64;  // keys per sub-tile
-constexpr int NTHREADS = 256;
-constexpr int K_WARP = 4, V_WARP = 5, QK_WARP = 6, PV_WARP = 7;
 constexpr int SMEM_PER_CTA = 115712;  // (228 KB - 2 x 1 KB reserved) / 2
 constexpr uint32_t TMEM_COLS = 256;  // two CTAs per SM share 512
 constexpr uint32_t COL_S = 0, COL_O = 128;
@@ -74,82 +70,6 @@ struct Layout {
   }
   __host__ __device__ uint32_t bytes() const { return misc_off + 16 + 1024; }  // + alignment
 };
-
-// Position in a ring of stages: slot, and the parity of its current round.
-struct Ring {
-  int slot = 0;
-  uint32_t round = 0;
-  __device__ __forceinline__ void next(int stages) {
-    if (++slot == stages) {
-      slot = 0;
-      round ^= 1u;
-    }
-  }
-};
-
-// 5-D tiled TMA load into this CTA's shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_5d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
-                                            int c3, int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// Where the boxes of a sub-tile lie: lane i looks up box i % boxes, one
-// sub-tile ahead of its loads (a block table's entry arrives meanwhile).
-struct Place {
-  int page, row;  // page < 0: behind the last key, nothing to load
-};
-__device__ __forceinline__ Place place_of(const CacheGeom &g, int b, int key, int end) {
-  if (key >= end) return Place{-1, 0};
-  if (g.block_table == nullptr) return Place{b, key};
-  const int j = key / g.page_size;
-  return Place{g.block_table[static_cast<int64_t>(b) * g.max_pages + j], key - j * g.page_size};
-}
-
-struct Plan {
-  int len, n, total, tiles;  // context keys, nodes, keys, sub-tiles
-  bool ok;
-};
-
-__device__ __forceinline__ Plan sequence_plan(const TreeArgs &a, int b) {
-  Plan p;
-  p.len = a.lens[b];
-  p.n = a.n_nodes != nullptr ? a.n_nodes[b] : a.T;
-  p.ok = p.len >= 0 && p.n >= 0 && p.n <= a.T && static_cast<int64_t>(p.len) + p.n <= cache_capacity(a.cache);
-  p.total = p.ok ? p.len + p.n : 0;
-  p.tiles = (p.total + SUB - 1) / SUB;
-  return p;
-}
-
-// Splits of a sequence: at most a.nsplit, each of at least MIN_TILES sub-tiles.
-constexpr int MIN_TILES = 4;
-__device__ __forceinline__ int sequence_splits(const TreeArgs &a, int tiles) {
-  const int most = (tiles + MIN_TILES - 1) / MIN_TILES;
-  return max(1, min(a.nsplit, most));
-}
-
-// Where row `row` (node * R + head) of KV head hk writes.
-__device__ __forceinline__ int64_t out_row(const TreeArgs &a, int b, int hk, int R, int row) {
-  return (static_cast<int64_t>(b) * a.T + row / R) * a.Hq + hk * R + row % R;
-}
-__device__ __forceinline__ float *out_lse(const TreeArgs &a, int b, int hk, int R, int row) {
-  return a.lse == nullptr ? nullptr : a.lse + (static_cast<int64_t>(b) * a.Hq + hk * R + row % R) * a.T + row / R;
-}
-
-// Full and boundary groups of the sub-tile at key k0, one group per lane:
-// bits 0-7 full, 8-15 boundary. Distances of the pairs that count lie in
-// [dmin, dmax]; with drafted keys in the sub-tile dmin is 0.
-__device__ __forceinline__ uint32_t tile_classes(int W, int G, int len, int deepest, int k0, int lane) {
-  const bool drafts = k0 + SUB > len;
-  const int64_t dmin = drafts ? 0 : static_cast<int64_t>(len) - (k0 + SUB - 1);
-  const int64_t dmax = static_cast<int64_t>(len) + deepest - min(k0, len);
-  const bool live = lane < G && dmin <= W;
-  const bool full = live && dmax <= W;
-  return __ballot_sync(FULL, full) | (__ballot_sync(FULL, live && !full) << 8);
-}
 
 // Columns c of su whose bit is clear become `fill`.
 __device__ __forceinline__ void keep_columns(uint32_t (&su)[64], uint64_t bits, uint32_t fill) {
@@ -191,8 +111,8 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   const int row0 = mt * a.tile_nodes * R;                            // first row of this CTA
   const int rows = min(a.tile_nodes, a.T - mt * a.tile_nodes) * R;  // up to 128
   const int warps = (rows + 31) / 32;                               // softmax warps with rows
-  const Plan plan = sequence_plan(a, b);
-  const int splits = sequence_splits(a, plan.tiles);
+  const Plan plan = sequence_plan<SUB>(a, b);
+  const int splits = sequence_splits<SUB>(a, plan.tiles);
   if (split >= splits) return;
   const int t_begin = static_cast<int>(static_cast<int64_t>(plan.tiles) * split / splits);
   const int nsub_all = static_cast<int>(static_cast<int64_t>(plan.tiles) * (split + 1) / splits) - t_begin;
@@ -227,64 +147,24 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
-  // The nodes: what each one sees (itself and its ancestors) and its depth, by
-  // pointer doubling: after step i a node has joined 2^i of its ancestors.
-  bool bad = !plan.ok;
-  if (warp == K_WARP) {
-    int j[2];
-    uint64_t m[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int t = lane + 32 * e;
-      j[e] = -1;
-      m[e] = t < plan.n ? 1ull << t : 0ull;
-      if (!bad && t < plan.n) {
-        const int p = a.parents[static_cast<int64_t>(b) * a.T + t];
-        if (p < -1 || p >= t)
-          bad = true;
-        else
-          j[e] = p;
-      }
-    }
-    bad = __any_sync(FULL, bad);
-    if (bad) j[0] = j[1] = -1;
-    while (__any_sync(FULL, j[0] >= 0 || j[1] >= 0)) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        sees[lane + 32 * e] = m[e];
-        jump[lane + 32 * e] = j[e];
-      }
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (j[e] >= 0) {
-          m[e] |= sees[j[e]];
-          j[e] = jump[j[e]];
-        }
-      __syncwarp();
-    }
-    int deep = 0;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int d = m[e] ? __popcll(m[e]) - 1 : 0;
-      sees[lane + 32 * e] = m[e];
-      depth[lane + 32 * e] = d;
-      deep = max(deep, d);
-    }
-    deep = __reduce_max_sync(FULL, deep);
-    if (lane == 0) *s_deepest = deep;
-  } else if (!bad && cg.block_table != nullptr) {
-    // a page outside the pool spoils this CTA's rows (its loads would return zeros)
-    const int other = threadIdx.x < K_WARP * 32 ? threadIdx.x : threadIdx.x - 32;
-    if (k_begin < k_end)
-      for (int64_t j = k_begin / cg.page_size + other; j <= (k_end - 1) / cg.page_size; j += NTHREADS - 32)
-        bad = bad || cache_page(cg, b, static_cast<int>(j * cg.page_size)) < 0;
-  }
   tc_fence_before();
-  bad = __syncthreads_or(bad);
+  __syncthreads();
   tc_fence_after();
+  const int box = a.box_rows;
+  const Work work{b, hk, k_begin, k_end, nsub_all, mt * a.tile_nodes, a.tile_nodes};
+  // The producers need no more than the lengths; the others look at the nodes
+  // and the pages meanwhile. A bad sequence raises the abort flag for them.
+  bool bad = !plan.ok;
+  if (warp == PV_WARP) bad = node_masks(a, plan, b, sees, depth, jump, s_deepest);
+  if (warp < 4) bad = bad || bad_page(cg, b, k_begin, k_end, threadIdx.x, 128);
+  if (warp != K_WARP && warp != V_WARP) {
+    bad = named_any(1, NTHREADS - 64, bad);
+    if (bad) *abort_flag = 1;
+  }
   const uint32_t tmem = *tmem_slot;
-  const int deepest = *s_deepest;
+  const int deepest = warp != K_WARP && warp != V_WARP ? *s_deepest : 0;
+  const int nsub = bad ? 0 : nsub_all;
+  const int my_cut = lane < G ? a.cut[lane] : 0;
   // The rows' place among the 128 lanes. A warp reaches the lanes of its own
   // quarter only, and warps w of both CTAs of an SM share a scheduler: few rows
   // go to other quarters in the CTA that got the upper half of TMEM, one warp of
@@ -292,89 +172,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   // issuers'.
   const int half = (tmem & 0xffffu) >= TMEM_COLS ? 1 : 0;
   const int warp0 = warps == 1 ? half : warps == 2 ? 2 * half : 0;
-  const int nsub = bad ? 0 : nsub_all;
-  const int my_cut = lane < G ? a.cut[lane] : 0;
-
-  const int box = a.box_rows, boxes = SUB / box;
-  const int first_key = k_begin + (lane & (boxes - 1)) * box;  // this lane's box of sub-tile 0
 
   if (warp == K_WARP) {
-    // ---------------------------------------------------- producer of Q, K
-    // One elected lane issues every copy, in a warp-uniform loop. A run of
-    // live groups goes in boxes of 4, 2 and 1 groups where a sub-tile is one
-    // box high (an issue costs about 100 cycles, whatever its size).
-    const bool leader = elect_one();
-    Ring ring;  // of the next load; a slot is free once its previous round was consumed
-    int issued = 0;
-    if (nsub > 0 && leader) {
-      mbar_arrive_expect_tx(q_full, G * 32u * R * a.tile_nodes);
-      for (int g = 0; g < G; ++g)
-        tma_load_4d(smem + L.q_off + g * L.q_tile, &tm.q, q_full, 16 * g, hk * R, mt * a.tile_nodes, b);
-    }
-    __syncwarp();
-    Place here = place_of(cg, b, first_key, k_end);
-    for (int u = 0; u < nsub; ++u) {
-      const Place next = place_of(cg, b, first_key + (u + 1) * SUB, k_end);
-      uint64_t *full = &k_full[ring.slot];
-      uint8_t *dst = smem + ring.slot * STAGE;
-      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
-      uint32_t need = (cls | (cls >> 8)) & 0xffu;
-      if (!KGM) need = ((need & 0xfu) ? 1u : 0u) | ((need >> 4) ? 2u : 0u);  // 64-dim chunks
-      if (u >= KST && !warp_wait_idle(&k_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) break;
-      const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
-      if (leader) mbar_arrive_expect_tx(full, have * __popc(need) * box * (KGM ? 32u : 128u));
-      for (int i = 0; i < have; ++i) {  // the boxes that exist come first
-        const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
-        if (leader) {
-          uint32_t left = need;
-          while (left) {
-            const int g = __ffs(left) - 1;
-            const uint32_t run = left >> g;
-            const int w = boxes > 1 ? 0 : KGM && (run & 0xfu) == 0xfu ? 2 : (run & 3u) == 3u ? 1 : 0;  // log2 of the box
-            if (KGM)
-              tma_load_5d(dst + g * K_TILE + i * box * 32, &tm.k[w], full, 0, row, g, hk, page);
-            else
-              tma_load_5d(dst + g * CHUNK + i * box * 128, &tm.k[w], full, 0, row, g, hk, page);
-            left &= ~(((1u << (1 << w)) - 1) << g);
-          }
-        }
-        __syncwarp();
-      }
-      ++issued;
-      ring.next(KST);
-      here = next;
-    }
-    // no bulk copy may still be in flight when this CTA's shared memory goes
-    if (nsub > 0) warp_wait_idle(q_full, 0, lim, nullptr);
-    for (int s = 0; s < KST && s < issued; ++s) {
-      const int last = s + ((issued - 1 - s) / KST) * KST;
-      warp_wait_idle(&k_full[s], (last / KST) & 1, lim, nullptr);
-    }
+    produce_k<D, KGM, SUB>(tm, a, work, plan.len, smem + L.q_off, L.q_tile, q_full, smem, k_full, k_empty, abort_flag);
   } else if (warp == V_WARP) {
-    // ------------------------------------------------------- producer of V
-    const bool leader = elect_one();
-    Ring ring;
-    int issued = 0;
-    Place here = place_of(cg, b, first_key, k_end);
-    for (int u = 0; u < nsub; ++u) {
-      const Place next = place_of(cg, b, first_key + (u + 1) * SUB, k_end);
-      uint64_t *full = &v_full[ring.slot];
-      if (u >= VST && !warp_wait_idle(&v_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) break;
-      const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
-      if (leader) mbar_arrive_expect_tx(full, have * box * D * 2u);
-      for (int i = 0; i < have; ++i) {
-        const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
-        if (leader) tma_load_5d(smem + L.v_off + ring.slot * STAGE + i * box * D * 2, &tm.v, full, 0, row, 0, hk, page);
-        __syncwarp();
-      }
-      ++issued;
-      ring.next(VST);
-      here = next;
-    }
-    for (int s = 0; s < VST && s < issued; ++s) {
-      const int last = s + ((issued - 1 - s) / VST) * VST;
-      warp_wait_idle(&v_full[s], (last / VST) & 1, lim, nullptr);
-    }
+    produce_v<D, SUB>(tm, a, work, smem + L.v_off, v_full, v_empty, abort_flag);
   } else if (warp == QK_WARP) {
     // --------------------------------------------------------- issuer of S
     // S(u) into half u & 1, once P V(u - 2) has read the P that lies there.
@@ -398,7 +200,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     };
     for (int u = 0; ok && u < nsub; ++u) {
       const int hh = u & 1;
-      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
+      const uint32_t cls = tile_classes<SUB>(my_cut, G, plan.len, deepest, k_begin + u * SUB, lane);
       const uint32_t s_col = tmem + COL_S + SUB * hh;
       const uint64_t kst_desc = k_desc + ((ring.slot * STAGE) >> 4);
       ok = warp_wait(&k_full[ring.slot], ring.round, lim, abort_flag) &&
@@ -444,8 +246,6 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     // V: dims contiguous (MN-major), one box after the other; in a box 8-key row
     // groups lie 1024 B apart and 64-dim chunks box * 128 B
     const uint64_t v_desc = smem_desc(smem_u32(smem + L.v_off), box * 128, 1024, SMEM_SWIZZLE_128B);
-    const uint32_t v_in = (box * 128) >> 4, v_step = box > 16 ? 2048 >> 4 : (D / 64) * v_in;  // 16 keys on
-    const uint32_t v_jump = box == 32 ? ((D / 64) * v_in - (4096 >> 4)) : 0u;               // from box 0 to box 1, beyond 2 steps
     Ring ring;
     for (int u = 0; u < nsub; ++u) {
       const int hh = u & 1;
@@ -456,7 +256,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
       if (leader) {
 #pragma unroll
         for (int kk = 0; kk < SUB / 16; ++kk)
-          umma_ts(tmem + COL_O, tmem + COL_S + SUB * hh + kk * 8, vst_desc + kk * v_step + (kk >= 2 ? v_jump : 0u), IDESC_PV,
+          umma_ts(tmem + COL_O, tmem + COL_S + SUB * hh + kk * 8, vst_desc + v_step<D>(kk, box), IDESC_PV,
                   (u > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&o_ready[hh]);
         umma_commit(&v_empty[ring.slot]);
@@ -478,14 +278,14 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const uint32_t o_addr = lane_addr + COL_O;
     const float c2 = a.scale_log2;
     const uint64_t c2x2 = pack_f2(c2, c2);
-    float m_run = -3.4028234663852886e38f, l_run = 0.f;  // base-2 units; finite, so that m - m is 0
+    float m_run = LOWEST, l_run = 0.f;  // base-2 units
     int bnd_cnt = 0;
     bool ok = nsub > 0;
     for (int u = 0; ok && u < nsub; ++u) {
       const int hh = u & 1;
       const int k0 = k_begin + u * SUB;
       const uint32_t s_addr = lane_addr + COL_S + SUB * hh;
-      const uint32_t cls = tile_classes(my_cut, G, plan.len, deepest, k0, lane);
+      const uint32_t cls = tile_classes<SUB>(my_cut, G, plan.len, deepest, k0, lane);
       const bool drafts = k0 + SUB > plan.len;
       if (cls >> 8) {
         int64_t prev = -1;
@@ -573,7 +373,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           *reinterpret_cast<uint4 *>(v + i * box * D * 2 + (p / 8) * box * 128 + (rr - i * box) * 128 + (p % 8) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_async_shared();
       }
       tc_fence_before();
       __syncwarp();
@@ -586,7 +386,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const bool done = ok && warp_wait(o_final, 0, lim, abort_flag);
     if (done) {
       tc_fence_after();
-      const float inv_l = l_run > 0.f ? 1.f / l_run : 0.f;
+      const float inv_l = l_run != 0.f ? 1.f / l_run : 0.f;
 #pragma unroll
       for (int c4 = 0; c4 < D / 32; ++c4) {
         uint32_t ov[32];
@@ -659,8 +459,8 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const 
   const int row = static_cast<int>(id % (a.T * R));
   const int hk = static_cast<int>(id / (a.T * R) % a.cache.Hkv);
   const int b = static_cast<int>(id / (a.T * R) / a.cache.Hkv);
-  const Plan plan = sequence_plan(a, b);
-  const int splits = sequence_splits(a, plan.tiles);
+  const Plan plan = sequence_plan<SUB>(a, b);
+  const int splits = sequence_splits<SUB>(a, plan.tiles);
   const float *lp = a.lse_part + id * a.nsplit;
   const float *op = a.o_part + id * a.nsplit * D + lane * E;
   float acc[E], sum = 0.f, M = -INFINITY;
@@ -703,19 +503,28 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const dim3 grid(a.row_tiles * a.nsplit, a.cache.Hkv, a.B);
   tree_kernel<D, KGM><<<grid, NTHREADS, smem, stream>>>(tm, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.nsplit == 1) return e;
-  const int64_t all_rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  tree_combine_kernel<D><<<static_cast<unsigned>((all_rows + COMBINE_WARPS - 1) / COMBINE_WARPS), COMBINE_WARPS * 32, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t combine(const TreeArgs &a, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
+  const unsigned blocks = static_cast<unsigned>((rows + COMBINE_WARPS - 1) / COMBINE_WARPS);
+  tree_combine_kernel<D><<<blocks, COMBINE_WARPS * 32, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_tree(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
+  if (tree_few_rows(a.T, a.Hq / a.cache.Hkv)) return launch_tree_few(tm, a, stream);
+  cudaError_t e;
   if (a.cache.D == 128)
-    return a.cache.k_group_major ? launch<128, true>(tm, a, stream) : launch<128, false>(tm, a, stream);
-  return a.cache.k_group_major ? launch<64, true>(tm, a, stream) : launch<64, false>(tm, a, stream);
+    e = a.cache.k_group_major ? launch<128, true>(tm, a, stream) : launch<128, false>(tm, a, stream);
+  else
+    e = a.cache.k_group_major ? launch<64, true>(tm, a, stream) : launch<64, false>(tm, a, stream);
+  if (e != cudaSuccess || a.nsplit == 1) return e;
+  return a.cache.D == 128 ? combine<128>(a, stream) : combine<64>(a, stream);
 }
 
 }  // namespace wp

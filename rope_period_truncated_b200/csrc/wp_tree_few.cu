@@ -1,0 +1,869 @@
+// Tree attention for few rows (nodes x query heads of a KV head <= 64), with
+// the products turned round: S^T = K Q^T and O^T = V^T P^T.
+//
+// The mathematics is that of wp_tree.cu. With few rows an M = 128 tile of
+// query rows would be mostly padding, and its exponentials would sit in one
+// warp, 64 per thread and sub-tile. Here the 128 rows of a product are keys
+// (S^T) or head dims (O^T) and the query rows are its N (32 or 64): the tensor
+// work shrinks with the rows, a softmax thread has one key and all rows, and
+// the four warps share a tile's exponentials evenly. HBM-bound.
+//
+// One CTA per SM. All (sequence, KV head) units lie end to end as a line of
+// 128-key tiles, cut evenly among the CTAs, whatever the lengths: a CTA walks
+// over its stretch in segments (what of one unit falls into it), and its loads
+// run ahead across them. Warps 4 and 5 fetch K and V, warp 6 issues S^T (M =
+// 128 keys, N = rows, one K = 16 product per live group, two buffers in TMEM),
+// warps 0-3 turn it into P^T (bf16, in shared memory: B of the second product,
+// rows contiguous), warp 7 issues O^T (M = 128 dims, V read as it lies,
+// MN-major). A segment that is a whole unit writes its rows; the others, at
+// most the first and the last of a CTA, write O (fp32) and LSE to the
+// workspace, and a second kernel merges them.
+//
+// The running maxima are one per row for the whole CTA, kept in shared memory,
+// and stay as they are while no logit exceeds them by more than 2^8: a tile
+// then needs only one vote. Otherwise (the first tile, and rarely later) the
+// exact maxima are formed with warp reductions and O^T and the sums rescaled.
+// Sums are kept per thread (its keys') and reduced once, at the end.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "wp_tree.cuh"
+
+namespace wp {
+namespace {
+
+constexpr int TILE = 128;
+constexpr int SMEM_CAP = 232448;  // dynamic shared memory of one CTA
+constexpr uint32_t GROUP = TILE * 32;   // 128 keys x 16 bf16 (group-major K)
+constexpr uint32_t CHUNK = TILE * 128;  // 128 keys x 64 bf16 (K in rows)
+constexpr int PAGE_FLAGS = 16;  // of segments: V is loaded up to TREE_MAX_STAGES tiles ahead of the softmax
+constexpr int TABLES = 4;  // of segments in flight: S runs at most two tiles ahead of the softmax
+constexpr uint32_t NUM_BARS = 4 + 4 * TREE_MAX_STAGES + 4 * 2 + TABLES + 5;
+
+// The nodes of one segment's sequence.
+struct NodeTable {
+  uint64_t sees[64];     // per node: the nodes it sees
+  uint64_t seen_by[64];  // per node: the rows that see it
+  uint64_t upto[64];     // per depth: the rows no deeper
+  int32_t depth[64];
+  int deepest, bad, pad[2];
+};
+
+// Shared memory: K ring, V ring, two P tiles, two Q (NR rows per group), then
+// the small tables and the barriers.
+template <int D, int NR>
+struct FewLayout {
+  static constexpr int G = D / 16;
+  static constexpr uint32_t STAGE = TILE * D * 2;
+  static constexpr uint32_t P_TILE = TILE * NR * 2;
+  static constexpr uint32_t Q_TILE = NR * 32;
+  static constexpr uint32_t Q_BYTES = G * Q_TILE;
+  // node tables, scratch, and per row: -max, rescaling, 4 warps' values
+  static constexpr uint32_t SMALL = TABLES * sizeof(NodeTable) + 64 * 4 + NR * 4 * 6;
+  static constexpr uint32_t FIXED = 2 * P_TILE + 2 * Q_BYTES + SMALL + NUM_BARS * 8 + 32 + PAGE_FLAGS * 4 + 1024;  // + alignment
+  uint32_t v_off, p_off, q_off, small_off, bar_off, misc_off;
+  __host__ __device__ FewLayout(int kst, int vst) {
+    v_off = kst * STAGE;
+    p_off = v_off + vst * STAGE;
+    q_off = p_off + 2 * P_TILE;
+    small_off = q_off + 2 * Q_BYTES;
+    bar_off = small_off + SMALL;
+    misc_off = bar_off + NUM_BARS * 8;  // abort flag, TMEM base, start of the stretch; from 32: page flags
+  }
+};
+
+// The line of tiles. Sequence b has plan.tiles tiles per KV head; prefix[b] is
+// the sum over the sequences before it. CTA c of G takes the tiles [cut(c),
+// cut(c + 1)).
+__device__ __forceinline__ int64_t cut(int64_t tiles, int c, int G) {
+  // tiles * c / G without leaving 64 bits: tiles < 2^16 x 2^16 x 2^23
+  return tiles / G * c + tiles % G * c / G;
+}
+__device__ __forceinline__ int cta_of(int64_t tiles, int64_t x, int G) {
+  int c = static_cast<int>(x / max(tiles / G, static_cast<int64_t>(1)));
+  c = min(c, G - 1);
+  while (c > 0 && cut(tiles, c, G) > x) --c;
+  while (cut(tiles, c + 1, G) <= x) ++c;
+  return c;
+}
+
+// A sequence with no nodes has nothing to attend; one with bad lengths is left
+// to the merging kernel.
+__device__ __forceinline__ Plan few_plan(const TreeArgs &a, int b) {
+  Plan p = sequence_plan<TILE>(a, b);
+  if (!p.ok || p.n == 0) p.tiles = 0;
+  return p;
+}
+
+struct Segment {
+  Plan plan;
+  int b, hk, k_begin, tiles, index;  // index: count of the CTA's segments
+  int slot;                          // of its partial result; -1: the whole unit
+};
+
+// One warp's walk over the CTA's segments.
+struct Walk {
+  int64_t x, x1;
+  int b, hk, t, cta, index;
+  bool first;
+  Plan plan;
+  __device__ __forceinline__ bool next(const TreeArgs &a, Segment &s) {
+    if (x >= x1) return false;
+    while (t >= plan.tiles) {  // on to the next unit that has tiles
+      t = 0;
+      if (plan.tiles > 0 && ++hk < a.cache.Hkv) break;
+      hk = 0;
+      plan = few_plan(a, ++b);
+    }
+    const int64_t left = x1 - x;
+    s.plan = plan;
+    s.b = b;
+    s.hk = hk;
+    s.tiles = static_cast<int>(left < plan.tiles - t ? left : plan.tiles - t);
+    s.k_begin = t * TILE;
+    s.index = index++;
+    s.slot = t == 0 && s.tiles == plan.tiles ? -1 : 2 * cta + (first ? 0 : 1);
+    first = false;
+    t += s.tiles;
+    x += s.tiles;
+    return true;
+  }
+};
+
+// TMEM columns [0, N) of this warp's lanes.
+template <int N>
+__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 64) {
+    tmem_ld64(taddr, r);
+  } else {
+    tmem_ld32(taddr, r);
+    tmem_wait_ld(r);
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&r)[N]) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) tmem_st32(taddr + c, *reinterpret_cast<const uint32_t(*)[32]>(&r[c]));
+  tmem_wait_st();
+}
+
+// Columns whose bit is clear become `fill`.
+template <int N>
+__device__ __forceinline__ void keep_rows(uint32_t (&r)[N], uint64_t bits, uint32_t fill) {
+  const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) r[c] = fill;
+}
+
+// Floats as integers of the same order (and back).
+__device__ __forceinline__ int ordered(uint32_t x) {
+  const int i = static_cast<int>(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+
+template <int D, bool KGM, int NR>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    tree_few_kernel(const __grid_constant__ TreeMaps tm, const __grid_constant__ TreeArgs a) {
+  using L = FewLayout<D, NR>;
+  constexpr int G = D / 16;
+  constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, NR, false, false);
+  constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, NR, true, true);
+  constexpr uint32_t TMEM_COLS = NR == 64 ? 256 : 128;  // S^T twice, O^T
+  constexpr uint32_t COL_O = 2 * NR;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const L lay(a.k_stages, a.v_stages);
+  NodeTable *tables = reinterpret_cast<NodeTable *>(smem + lay.small_off);
+  int32_t *jump = reinterpret_cast<int32_t *>(tables + TABLES);
+  float *negm = reinterpret_cast<float *>(jump + 64), *alpha = negm + NR;  // minus the running maxima; rescaling
+  float *part4 = alpha + NR;                                               // [4][NR] of the warps
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.bar_off);
+  uint64_t *q_full = bars, *q_empty = q_full + 2, *k_full = q_empty + 2, *k_empty = k_full + TREE_MAX_STAGES,
+           *v_full = k_empty + TREE_MAX_STAGES, *v_empty = v_full + TREE_MAX_STAGES, *s_ready = v_empty + TREE_MAX_STAGES,
+           *s_free = s_ready + 2, *p_ready = s_free + 2, *o_ready = p_ready + 2, *t_ready = o_ready + 2,
+           *o_final = t_ready + TABLES, *bnd_ready = o_final + 1, *bnd_done = bnd_ready + 1, *drain = bnd_done + 1;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + lay.misc_off);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lay.misc_off + 4);
+  volatile int *bad_pages = reinterpret_cast<volatile int *>(smem + lay.misc_off + 32);  // set by the V producer
+  int *start = reinterpret_cast<int *>(smem + lay.misc_off + 8);                         // sequence, KV head, tile
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const CacheGeom &cg = a.cache;
+  const int R = a.Hq / cg.Hkv, rows = a.T * R;
+  const long long lim = a.wait_limit;
+  const int my_cut = lane < G ? a.cut[lane] : 0;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < TABLES; ++s) mbar_init(&t_ready[s], 1);
+    for (int s = 0; s < a.k_stages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < a.v_stages; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&s_ready[s], 1);
+      mbar_init(&s_free[s], 4);
+      mbar_init(&p_ready[s], 4);
+      mbar_init(&o_ready[s], 1);
+      mbar_init(&drain[s], 1);
+    }
+    mbar_init(o_final, 1);
+    mbar_init(bnd_ready, 1);
+    mbar_init(bnd_done, 4);
+    fence_barrier_init();
+  }
+  if (warp == QK_WARP) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  // rows of Q beyond the last one, as zeros (their columns of S^T take part in the votes)
+  const int pad = (NR - rows) * 2;  // 16-byte pieces per group
+  for (int e = threadIdx.x; e < pad * G * 2; e += NTHREADS)
+    *reinterpret_cast<uint4 *>(smem + lay.q_off + (e / pad) * L::Q_TILE + rows * 32 + (e % pad) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  fence_async_shared();
+
+  // The line of tiles: each thread takes a run of sequences; the sums before
+  // them by a scan over the block. CTA 0 writes them down for the merge.
+  Walk walk;
+  {
+    const int run = (a.B + NTHREADS - 1) / NTHREADS, b0 = min(static_cast<int>(threadIdx.x) * run, a.B), b1 = min(b0 + run, a.B);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += few_plan(a, b).tiles;
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(FULL, inc, o);
+      if (lane >= o) inc += y;
+    }
+    int64_t *sums = reinterpret_cast<int64_t *>(part4);  // 8 warps
+    if (lane == 31) sums[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t before = inc - mine, total = 0;
+    for (int w = 0; w < NTHREADS / 32; ++w) {
+      before += w < warp ? sums[w] : 0;
+      total += sums[w];
+    }
+    const int64_t tiles = total * cg.Hkv;
+    walk.x = cut(tiles, blockIdx.x, gridDim.x);
+    walk.x1 = cut(tiles, blockIdx.x + 1, gridDim.x);
+    for (int b = b0; b < b1; ++b) {
+      const int t = few_plan(a, b).tiles;
+      if (blockIdx.x == 0 && a.prefix != nullptr) a.prefix[b] = before;
+      const int64_t at = walk.x - before * cg.Hkv;  // the stretch's start within sequence b
+      if (at >= 0 && at < static_cast<int64_t>(t) * cg.Hkv) {
+        start[0] = b;
+        start[1] = static_cast<int>(at / t);
+        start[2] = static_cast<int>(at % t);
+      }
+      before += t;
+    }
+    if (blockIdx.x == 0 && a.prefix != nullptr && threadIdx.x == NTHREADS - 1) a.prefix[a.B] = total;
+    __syncthreads();
+    walk.cta = blockIdx.x;
+    walk.index = 0;
+    walk.first = true;
+    if (walk.x < walk.x1) {
+      walk.b = start[0];
+      walk.hk = start[1];
+      walk.t = start[2];
+      walk.plan = few_plan(a, walk.b);
+    }
+  }
+  const uint32_t tmem = *tmem_slot;
+  const int box = a.box_rows, boxes = TILE / box;
+  Segment seg;
+
+  if (warp == K_WARP) {
+    // ---------------------------------------------------- producer of Q, K
+    // One elected lane issues every copy, in a warp-uniform loop; lane i looks
+    // up box i % boxes one tile ahead. A run of live groups goes in boxes of 4,
+    // 2 and 1 groups where a tile is one box high (an issue costs about 100
+    // cycles, whatever its size).
+    const bool leader = elect_one();
+    Ring ring;
+    int issued = 0, q_issued = 0;
+    bool ok = true;
+    while (ok && walk.next(a, seg)) {
+      const int qs = seg.index & 1;
+      if (seg.index >= 2 && !warp_wait_idle(&q_empty[qs], ((seg.index >> 1) - 1) & 1, lim, abort_flag)) break;
+      if (leader) {
+        mbar_arrive_expect_tx(&q_full[qs], G * 32u * rows);
+        for (int g = 0; g < G; ++g)
+          tma_load_4d(smem + lay.q_off + qs * L::Q_BYTES + g * L::Q_TILE, &tm.q, &q_full[qs], 16 * g, seg.hk * R, 0, seg.b);
+      }
+      __syncwarp();
+      ++q_issued;
+      const int end = min(seg.k_begin + seg.tiles * TILE, seg.plan.total);
+      const int key0 = seg.k_begin + (lane & (boxes - 1)) * box;
+      Place here = place_of(cg, seg.b, key0, end);
+      for (int u = 0; u < seg.tiles; ++u) {
+        const Place next = place_of(cg, seg.b, key0 + (u + 1) * TILE, end);
+        uint64_t *full = &k_full[ring.slot];
+        uint8_t *dst = smem + ring.slot * L::STAGE;
+        uint32_t need = live_groups<TILE>(my_cut, G, seg.plan.len, seg.k_begin + u * TILE, lane);
+        if (!KGM) need = ((need & 0xfu) ? 1u : 0u) | ((need >> 4) ? 2u : 0u);  // 64-dim chunks
+        if (issued >= a.k_stages && !warp_wait_idle(&k_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int have = __popc(__ballot_sync(FULL, lane < boxes && key0 + u * TILE < end));
+        if (leader) mbar_arrive_expect_tx(full, have * __popc(need) * box * (KGM ? 32u : 128u));
+        for (int i = 0; i < have; ++i) {
+          const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
+          if (leader) {
+            uint32_t left = need;
+            while (left) {
+              const int g = __ffs(left) - 1;
+              const uint32_t run = left >> g;
+              const int wide = boxes > 1 ? 0 : KGM && (run & 0xfu) == 0xfu ? 2 : (run & 3u) == 3u ? 1 : 0;  // log2 of the box
+              tma_load_5d(dst + (KGM ? g * GROUP + i * box * 32 : g * CHUNK + i * box * 128), &tm.k[wide], full, 0, row, g,
+                          seg.hk, page);
+              left &= ~(((1u << (1 << wide)) - 1) << g);
+            }
+          }
+          __syncwarp();
+        }
+        ++issued;
+        ring.next(a.k_stages);
+        here = next;
+      }
+    }
+    // no bulk copy may still be in flight when this CTA's shared memory goes
+    for (int s = 0; s < 2 && s < q_issued; ++s) {
+      const int last = s + ((q_issued - 1 - s) / 2) * 2;
+      warp_wait_idle(&q_full[s], (last / 2) & 1, lim, nullptr);
+    }
+    for (int s = 0; s < a.k_stages && s < issued; ++s) {
+      const int last = s + ((issued - 1 - s) / a.k_stages) * a.k_stages;
+      warp_wait_idle(&k_full[s], (last / a.k_stages) & 1, lim, nullptr);
+    }
+  } else if (warp == V_WARP) {
+    // ------------------------------------------------------- producer of V
+    // It also looks at the pages: an entry outside the pool spoils the segment
+    // (TMA reads nothing there and gives zeros).
+    const bool leader = elect_one();
+    Ring ring;
+    int issued = 0;
+    bool ok = true;
+    while (ok && walk.next(a, seg)) {
+      const int end = min(seg.k_begin + seg.tiles * TILE, seg.plan.total);
+      const int key0 = seg.k_begin + (lane & (boxes - 1)) * box;
+      Place here = place_of(cg, seg.b, key0, end);
+      if (leader) bad_pages[seg.index % PAGE_FLAGS] = 0;
+      __syncwarp();
+      for (int u = 0; u < seg.tiles; ++u) {
+        const Place next = place_of(cg, seg.b, key0 + (u + 1) * TILE, end);
+        uint64_t *full = &v_full[ring.slot];
+        if (issued >= a.v_stages && !warp_wait_idle(&v_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const bool mine = lane < boxes && key0 + u * TILE < end;
+        const int have = __popc(__ballot_sync(FULL, mine));
+        const bool bad = __any_sync(FULL, mine && (here.page < 0 || here.page >= cg.n_pages));
+        if (leader) {
+          if (bad) bad_pages[seg.index % PAGE_FLAGS] = 1;
+          mbar_arrive_expect_tx(full, have * box * D * 2u);
+        }
+        for (int i = 0; i < have; ++i) {
+          const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
+          if (leader) tma_load_5d(smem + lay.v_off + ring.slot * L::STAGE + i * box * D * 2, &tm.v, full, 0, row, 0, seg.hk, page);
+          __syncwarp();
+        }
+        ++issued;
+        ring.next(a.v_stages);
+        here = next;
+      }
+    }
+    for (int s = 0; s < a.v_stages && s < issued; ++s) {
+      const int last = s + ((issued - 1 - s) / a.v_stages) * a.v_stages;
+      warp_wait_idle(&v_full[s], (last / a.v_stages) & 1, lim, nullptr);
+    }
+  } else if (warp == QK_WARP) {
+    // ------------------------------------------------------- issuer of S^T
+    const bool leader = elect_one();
+    const uint64_t q_desc0 = smem_desc(smem_u32(smem + lay.q_off), 16, 256, SMEM_SWIZZLE_32B);
+    const uint64_t k_desc = KGM ? smem_desc(smem_u32(smem), 16, 256, SMEM_SWIZZLE_32B)
+                                : smem_desc(smem_u32(smem), 16, 1024, SMEM_SWIZZLE_128B);
+    Ring ring;
+    int bnd_cnt = 0, it = 0;  // it: tiles of all segments
+    bool ok = true;
+    while (ok && walk.next(a, seg)) {
+      const int qs = seg.index & 1;
+      const uint64_t q_desc = q_desc0 + ((qs * L::Q_BYTES) >> 4);
+      const auto issue_groups = [&](uint32_t s_col, uint64_t kst_desc, uint32_t groups, uint32_t acc) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          if (groups & (1u << g)) {
+            // K in rows: group g is 32 bytes into the 128-byte rows of chunk g / 4
+            const uint32_t koff = KGM ? g * GROUP : (g / 4) * CHUNK + (g % 4) * 32;
+            umma_ss(s_col, kst_desc + (koff >> 4), q_desc + g * (L::Q_TILE >> 4), IDESC_QK, acc);
+            acc = 1;
+          }
+      };
+      // The nodes' table. The softmax has taken S^T of two tiles ago, so it is
+      // at most two segments back, and this table's last reader is done.
+      ok = it < 2 || warp_wait(&s_free[it & 1], ((it >> 1) - 1) & 1, lim, abort_flag);
+      if (!ok) break;
+      NodeTable &tab = tables[seg.index % TABLES];
+      const bool bad = node_masks(a, seg.plan, seg.b, tab.sees, tab.depth, jump, &tab.deepest);
+      __syncwarp();
+      const int deepest = tab.deepest;
+      {
+        const int r0 = lane, r1 = lane + 32;
+        const uint64_t m0 = r0 < rows ? tab.sees[r0 / R] : 0ull, m1 = r1 < rows ? tab.sees[r1 / R] : 0ull;
+        const int d0 = r0 < rows ? tab.depth[r0 / R] : 64, d1 = r1 < rows ? tab.depth[r1 / R] : 64;
+        for (int u = 0; u < seg.plan.n; ++u) {
+          const uint64_t lo = __ballot_sync(FULL, (m0 >> u) & 1), hi = __ballot_sync(FULL, (m1 >> u) & 1);
+          if (lane == 0) tab.seen_by[u] = hi << 32 | lo;
+        }
+        for (int u = 0; u <= deepest; ++u) {
+          const uint64_t lo = __ballot_sync(FULL, d0 <= u), hi = __ballot_sync(FULL, d1 <= u);
+          if (lane == 0) tab.upto[u] = hi << 32 | lo;
+        }
+        if (lane == 0) tab.bad = bad;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&t_ready[seg.index % TABLES]);
+      }
+      ok = warp_wait(&q_full[qs], (seg.index >> 1) & 1, lim, abort_flag);
+      for (int u = 0; ok && u < seg.tiles; ++u, ++it) {
+        const int hh = it & 1;
+        const uint32_t cls = tile_classes<TILE>(my_cut, G, seg.plan.len, deepest, seg.k_begin + u * TILE, lane);
+        const uint32_t s_col = tmem + NR * hh;
+        const uint64_t kst_desc = k_desc + ((ring.slot * L::STAGE) >> 4);
+        ok = warp_wait(&k_full[ring.slot], ring.round, lim, abort_flag) &&
+             (it < 2 || u == 0 || warp_wait(&s_free[hh], ((it >> 1) - 1) & 1, lim, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t acc = 0;
+        const uint32_t bnd = cls >> 8;
+        if (bnd) {
+          // boundary classes first, ascending cutoff; each one masked in place
+          int64_t prev = -1;
+          int32_t W;
+          uint32_t groups;
+          while (ok && next_boundary_class(a.cut, bnd, prev, &W, &groups)) {
+            if (leader) {
+              issue_groups(s_col, kst_desc, groups, acc);
+              umma_commit(bnd_ready);
+            }
+            acc = 1;
+            __syncwarp();
+            ok = warp_wait(bnd_done, bnd_cnt & 1, lim, abort_flag);
+            tc_fence_after();
+            ++bnd_cnt;
+            prev = W;
+          }
+          if (!ok) break;
+        }
+        if (leader) {
+          issue_groups(s_col, kst_desc, cls & 0xffu, acc);
+          umma_commit(&s_ready[hh]);
+          umma_commit(&k_empty[ring.slot]);
+          if (u == seg.tiles - 1) umma_commit(&q_empty[qs]);
+        }
+        __syncwarp();
+        ring.next(a.k_stages);
+      }
+    }
+    // every product must have finished before TMEM is given back
+    if (leader) umma_commit(&drain[0]);
+    __syncwarp();
+    warp_wait(&drain[0], 0, lim, nullptr);
+  } else if (warp == PV_WARP) {
+    // ------------------------------------------------------- issuer of O^T
+    const bool leader = elect_one();
+    // A = V^T: dims contiguous (MN-major); 8-key row groups 1024 B and 64-dim
+    // chunks box * 128 B apart. At d = 64 there is one chunk, and the upper 64
+    // rows of O^T repeat the lower ones. B = P^T: rows contiguous.
+    const uint64_t v_desc = smem_desc(smem_u32(smem + lay.v_off), D == 128 ? box * 128 : 0, 1024, SMEM_SWIZZLE_128B);
+    const uint64_t p_desc = smem_desc(smem_u32(smem + lay.p_off), 0, 8 * NR * 2, NR == 64 ? SMEM_SWIZZLE_128B : SMEM_SWIZZLE_64B);
+    Ring ring;
+    int it = 0;
+    bool ok = true;
+    while (ok && walk.next(a, seg)) {
+      for (int u = 0; u < seg.tiles; ++u, ++it) {
+        const int hh = it & 1;
+        const uint64_t vst_desc = v_desc + ((ring.slot * L::STAGE) >> 4);
+        const uint64_t pst_desc = p_desc + ((hh * L::P_TILE) >> 4);
+        ok = warp_wait(&v_full[ring.slot], ring.round, lim, abort_flag) && warp_wait(&p_ready[hh], (it >> 1) & 1, lim, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < TILE / 16; ++kk)
+            umma_ss(tmem + COL_O, vst_desc + v_step<D>(kk, box), pst_desc + kk * ((16 * NR * 2) >> 4), IDESC_PV,
+                    (u > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&o_ready[hh]);
+          umma_commit(&v_empty[ring.slot]);
+          if (u == seg.tiles - 1) umma_commit(o_final);
+        }
+        __syncwarp();
+        ring.next(a.v_stages);
+      }
+    }
+    if (leader) umma_commit(&drain[1]);
+    __syncwarp();
+    warp_wait(&drain[1], 0, lim, nullptr);
+  } else {
+    // ------------------------------------------------------------- softmax
+    // The four warps meet in a vote on every tile, so none leaves the loop by
+    // itself: one whose wait gave up goes on to the vote and says so there.
+    const int kt = warp * 32 + lane;  // key of the tile == TMEM lane; head dim == lane of O^T
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t o_addr = lane_addr + COL_O;
+    const float c2 = a.scale_log2;
+    const uint64_t c2x2 = pack_f2(c2, c2);
+    uint64_t l2[NR / 2];  // this thread's sums, two rows each
+    int bnd_cnt = 0, it = 0;
+    bool ok = true;
+    Ring vr;  // the V stage of the tile
+    while (walk.next(a, seg)) {
+      const Plan &plan = seg.plan;
+      if (threadIdx.x < NR) negm[threadIdx.x] = -LOWEST;
+#pragma unroll
+      for (int i = 0; i < NR / 2; ++i) l2[i] = 0ull;
+      const NodeTable &tab = tables[seg.index % TABLES];
+      ok = ok && warp_wait(&t_ready[seg.index % TABLES], (seg.index / TABLES) & 1, lim, abort_flag);
+      named_sync(2, 128);
+      const int deepest = tab.deepest;
+      for (int u = 0; u < seg.tiles; ++u, ++it) {
+        const int hh = it & 1;
+        const int k0 = seg.k_begin + u * TILE, key = k0 + kt;
+        const uint32_t s_addr = lane_addr + NR * hh;
+        const uint32_t cls = tile_classes<TILE>(my_cut, G, plan.len, deepest, k0, lane);
+        const bool drafts = k0 + TILE > plan.len;
+        const bool context = key < plan.len, there = key < plan.total;
+        if (cls >> 8) {
+          const int64_t kpos = context || !there ? key : plan.len + tab.depth[key - plan.len];
+          int64_t prev = -1;
+          int32_t W;
+          uint32_t groups;
+          while (ok && next_boundary_class(a.cut, cls >> 8, prev, &W, &groups)) {
+            // rows within the window: len + depth - kpos <= W
+            const int64_t most = W + kpos - plan.len;
+            const uint64_t keep = most < 0 ? 0ull : tab.upto[static_cast<int>(min(most, static_cast<int64_t>(deepest)))];
+            ok = warp_wait(bnd_ready, bnd_cnt & 1, lim, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t su[NR];
+            load_columns<NR>(s_addr, su);
+            keep_rows<NR>(su, keep, 0u);
+            store_columns<NR>(s_addr, su);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bnd_done);
+            ++bnd_cnt;
+            prev = W;
+          }
+        }
+        ok = ok && warp_wait(&s_ready[hh], (it >> 1) & 1, lim, abort_flag);
+        tc_fence_after();
+        uint32_t su[NR];
+        if (cls == 0) {  // no product: zeros, by the same load
+#pragma unroll
+          for (int c = 0; c < NR; ++c) su[c] = 0u;
+          store_columns<NR>(s_addr, su);
+        }
+        load_columns<NR>(s_addr, su);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[hh]);
+        if (drafts) keep_rows<NR>(su, context ? ~0ull : there ? tab.seen_by[key - plan.len] : 0ull, 0xff800000u);
+        // Does any logit exceed its row's maximum by more than 2^8?
+        float over = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NR; c += 4) {
+          const float4 m4 = *reinterpret_cast<const float4 *>(negm + c);
+          float x0, x1, x2, x3;
+          unpack_f2(ffma2(pack_f2(__uint_as_float(su[c]), __uint_as_float(su[c + 1])), c2x2, pack_f2(m4.x, m4.y)), x0, x1);
+          unpack_f2(ffma2(pack_f2(__uint_as_float(su[c + 2]), __uint_as_float(su[c + 3])), c2x2, pack_f2(m4.z, m4.w)), x2, x3);
+          over = max3(over, max3(x0, x1, x2), x3);
+        }
+        if (named_any(2, 128, over > RESCALE_THRESHOLD || !ok)) {
+          if (named_any(2, 128, !ok)) {
+            ok = false;
+            break;
+          }
+          int *warp_max = reinterpret_cast<int *>(part4) + warp * NR;
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            const int mx = __reduce_max_sync(FULL, ordered(su[c]));
+            if (lane == (c & 31)) warp_max[c] = mx;
+          }
+          named_sync(2, 128);
+          if (threadIdx.x < NR) {
+            const int *p = reinterpret_cast<const int *>(part4) + threadIdx.x;
+            const int mx = max(max(p[0], p[NR]), max(p[2 * NR], p[3 * NR]));
+            const float m_old = -negm[threadIdx.x];
+            const float m_new = fmaxf(m_old, __int_as_float(ordered(static_cast<uint32_t>(mx))) * c2);
+            alpha[threadIdx.x] = fast_exp2(m_old - m_new);
+            negm[threadIdx.x] = -m_new;
+          }
+          named_sync(2, 128);
+          if (u > 0) {
+#pragma unroll
+            for (int c = 0; c < NR; c += 2) {
+              float l0, l1;
+              unpack_f2(l2[c / 2], l0, l1);
+              l2[c / 2] = pack_f2(l0 * alpha[c], l1 * alpha[c + 1]);
+            }
+            ok = warp_wait(&o_ready[hh ^ 1], ((it - 1) >> 1) & 1, lim, abort_flag);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < NR; c0 += 32) {
+              uint32_t ov[32];
+              tmem_ld32(o_addr + c0, ov);
+              tmem_wait_ld(ov);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha[c0 + c]);
+              tmem_st32(o_addr + c0, ov);
+            }
+            tmem_wait_st();
+          }
+        }
+        // P^T of two tiles ago must have been read before its place is written again
+        if (it >= 2) ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag) && ok;
+        uint8_t *p_row = smem + lay.p_off + hh * L::P_TILE + kt * (NR * 2);
+        const int turn = NR == 64 ? (kt & 7) : ((kt >> 1) & 3);  // the swizzle of the row's 16-byte pieces
+#pragma unroll
+        for (int c = 0; c < NR; c += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t m2 = *reinterpret_cast<const uint64_t *>(negm + c + 2 * e);
+            float x0, x1;
+            unpack_f2(ffma2(pack_f2(__uint_as_float(su[c + 2 * e]), __uint_as_float(su[c + 2 * e + 1])), c2x2, m2), x0, x1);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            l2[c / 2 + e] = fadd2(l2[c / 2 + e], pack_f2(p0, p1));
+            w[e] = pack_bf16x2(p0, p1);
+          }
+          *reinterpret_cast<uint4 *>(p_row + (((c >> 3) ^ turn) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (u == seg.tiles - 1) {
+          // The last tile: V has landed (so have the V producer's words on the
+          // pages), and its rows behind the last key become zeros: unused slots
+          // may hold anything.
+          ok = warp_wait(&v_full[vr.slot], vr.round, lim, abort_flag) && ok;
+          if (!there) {
+            const int i = kt / box;
+            uint8_t *v = smem + lay.v_off + vr.slot * L::STAGE + i * box * D * 2 + (kt - i * box) * 128;
+#pragma unroll
+            for (int p = 0; p < D / 8; ++p)
+              *reinterpret_cast<uint4 *>(v + (p / 8) * box * 128 + (p % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        vr.next(a.v_stages);
+        fence_async_shared();
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&p_ready[hh]);
+      }
+      // ---------------------------------------------------------- epilogue
+      ok = ok && warp_wait(o_final, seg.index & 1, lim, abort_flag);
+      ok = !named_any(2, 128, !ok);  // all four warps or none
+      if (!ok) *abort_flag = 1;
+      const bool spoilt = !ok || tab.bad || bad_pages[seg.index % PAGE_FLAGS];
+      if (ok) {
+        // the rows' sums over the four warps' keys
+#pragma unroll
+        for (int c = 0; c < NR; c += 2) {
+          float l0, l1;
+          unpack_f2(l2[c / 2], l0, l1);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) {
+            l0 += __shfl_xor_sync(FULL, l0, o);
+            l1 += __shfl_xor_sync(FULL, l1, o);
+          }
+          if (lane == 0) *reinterpret_cast<float2 *>(part4 + warp * NR + c) = make_float2(l0, l1);
+        }
+        tc_fence_after();
+      }
+      named_sync(2, 128);
+      if (threadIdx.x < rows) {
+        const int r = threadIdx.x, node = r / R;
+        const float l = ok ? (part4[r] + part4[NR + r]) + (part4[2 * NR + r] + part4[3 * NR + r]) : 0.f;
+        const float m = -negm[r];
+        const bool live = node < plan.n;
+        // rows of nodes that are not there are 0, a spoilt segment's NaN
+        alpha[r] = spoilt ? __int_as_float(0x7FC00000) : live && l != 0.f ? 1.f / l : 0.f;
+        if (seg.slot >= 0)
+          a.lse_part[static_cast<int64_t>(seg.slot) * rows + r] = spoilt ? INFINITY : m + __log2f(l);
+        else if (a.lse != nullptr)
+          a.lse[(static_cast<int64_t>(seg.b) * a.Hq + seg.hk * R + r - node * R) * a.T + node] =
+              spoilt ? __int_as_float(0x7FC00000) : live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      }
+      named_sync(2, 128);
+      // Lanes are head dims: 32 contiguous values of a row per warp. In the
+      // workspace the rows follow one another; in o a node's R heads do.
+      const int64_t base = seg.slot >= 0 ? static_cast<int64_t>(seg.slot) * rows * D
+                                         : (static_cast<int64_t>(seg.b) * a.T * a.Hq + seg.hk * R) * D;
+      const int64_t jump_node = static_cast<int64_t>(a.Hq - R) * D;  // beyond the R heads of a node
+      int64_t at = base + kt;
+      int head = 0;
+#pragma unroll 1
+      for (int c0 = 0; c0 < rows; c0 += 32) {
+        uint32_t ov[32];
+        tmem_ld32(o_addr + c0, ov);
+        tmem_wait_ld(ov);
+        if (kt < D) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < rows) {
+              const float f = alpha[c0 + c];
+              // a row that sees nothing is 0, whatever the accumulator holds
+              const float v = f == 0.f ? 0.f : __uint_as_float(ov[c]) * f;
+              if (seg.slot >= 0) {
+                a.o_part[at] = v;
+              } else {
+                a.o[at] = __float2bfloat16_rn(v);
+                if (++head == R) {
+                  head = 0;
+                  at += jump_node;
+                }
+              }
+              at += D;
+            }
+        }
+      }
+      tc_fence_before();
+      named_sync(2, 128);  // part4, alpha and negm are free again
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == QK_WARP) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Merges the partial results of the units that more than one CTA worked on, one
+// warp per row: O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M). It also
+// writes the rows that no CTA had: of sequences without nodes, or with bad
+// lengths.
+constexpr int MERGE_WARPS = 4;
+
+template <int D>
+__global__ void __launch_bounds__(MERGE_WARPS * 32) tree_few_merge_kernel(const __grid_constant__ TreeArgs a, int G) {
+  constexpr int E = D / 32;
+  cudaGridDependencySynchronize();
+  const int R = a.Hq / a.cache.Hkv, rows = a.T * R;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * MERGE_WARPS + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (id >= static_cast<int64_t>(a.B) * a.cache.Hkv * rows) return;
+  const int row = static_cast<int>(id % rows);
+  const int64_t unit = id / rows;
+  const int hk = static_cast<int>(unit % a.cache.Hkv), b = static_cast<int>(unit / a.cache.Hkv);
+  const int64_t before = a.prefix[b], own = a.prefix[b + 1] - before, tiles = a.prefix[a.B] * a.cache.Hkv;
+  float acc[E], sum = 1.f, M = 0.f;
+  bool spoilt = false, live = false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  if (own == 0) {
+    spoilt = !sequence_plan<TILE>(a, b).ok;
+  } else {
+    const int64_t x0 = before * a.cache.Hkv + own * hk;
+    const int c0 = cta_of(tiles, x0, G), c1 = cta_of(tiles, x0 + own - 1, G);
+    if (c0 == c1) return;  // that CTA wrote the rows
+    // CTA c's slot: its first segment, or for a unit that begins within c0 its last
+    const int late = cut(tiles, c0, G) < x0 ? 1 : 0;
+    const auto slot_of = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? late : 0)) * rows + row; };
+    // with fewer tiles than CTAs some of them have none
+    const auto has = [&](int c) { return c <= c1 && cut(tiles, c, G) < cut(tiles, c + 1, G); };
+    live = row / R < (a.n_nodes != nullptr ? a.n_nodes[b] : a.T);
+    M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32)
+      if (has(c)) M = fmaxf(M, a.lse_part[slot_of(c)]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    spoilt = M == INFINITY;
+    sum = 0.f;
+    for (int c = c0; c <= c1; c += 4) {
+      float w[4], v[4][E];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = has(c + k);
+        const int64_t s = slot_of(in ? c + k : c0);  // c0 has a slot
+        const float l = a.lse_part[s];
+        w[k] = !in || l == -INFINITY ? 0.f : fast_exp2(l - M);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = a.o_part[s * D + lane * E + e];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum += w[k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += w[k] * v[k][e];
+      }
+    }
+  }
+  __nv_bfloat16 *o = a.o + out_row(a, b, hk, R, row) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const float x = spoilt ? __int_as_float(0x7fc00000) : live ? acc[e] / sum : 0.f;
+    const float y = spoilt ? __int_as_float(0x7fc00000) : live ? acc[e + 1] / sum : 0.f;
+    *reinterpret_cast<uint32_t *>(o + e) = pack_bf16x2(x, y);
+  }
+  float *lse = out_lse(a, b, hk, R, row);
+  if (lane == 0 && lse != nullptr)
+    *lse = spoilt ? __int_as_float(0x7fc00000) : live ? (M + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+template <int D, bool KGM, int NR>
+cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
+  using L = FewLayout<D, NR>;
+  // as many stages as fit, one more of K than of V where the number is odd
+  const int fit = (SMEM_CAP - static_cast<int>(L::FIXED)) / static_cast<int>(L::STAGE);
+  const int stages = fit < 2 * TREE_MAX_STAGES ? fit : 2 * TREE_MAX_STAGES;
+  a.v_stages = stages / 2;
+  a.k_stages = stages - a.v_stages;
+  const int smem = static_cast<int>(L::FIXED + stages * L::STAGE);
+  cudaError_t e = cudaFuncSetAttribute(tree_few_kernel<D, KGM, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  tree_few_kernel<D, KGM, NR><<<a.nsplit, NTHREADS, smem, stream>>>(tm, a);
+  return cudaGetLastError();
+}
+
+template <int D, bool KGM>
+cudaError_t launch_rows(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
+  return a.T * (a.Hq / a.cache.Hkv) <= 32 ? launch<D, KGM, 32>(tm, a, stream) : launch<D, KGM, 64>(tm, a, stream);
+}
+
+template <int D>
+cudaError_t launch_both(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
+  const cudaError_t e = a.cache.k_group_major ? launch_rows<D, true>(tm, a, stream) : launch_rows<D, false>(tm, a, stream);
+  if (e != cudaSuccess) return e;
+  // started while the first kernel runs; it waits for its results on the device
+  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + MERGE_WARPS - 1) / MERGE_WARPS));
+  cfg.blockDim = dim3(MERGE_WARPS * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_few_merge_kernel<D>, a, a.nsplit);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_few(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
+  return a.cache.D == 128 ? launch_both<128>(tm, a, stream) : launch_both<64>(tm, a, stream);
+}
+
+}  // namespace wp
