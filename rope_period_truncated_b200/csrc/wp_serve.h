@@ -118,15 +118,14 @@ struct TreeArgs {
   long long wait_limit;
 };
 
-// How the work is cut. Up to 64 rows per KV head (R query heads of T nodes) go
+// How the work is cut. Up to 32 rows per KV head (R query heads of T nodes) go
 // to the kernel whose products have keys and dims as their 128 rows: tiles of
 // 128 keys, one CTA per SM, the tiles of all sequences and KV heads dealt out
 // evenly. More rows go to the one that has query rows there: tiles of whole
-// nodes, 64 keys, two CTAs per SM, each (sequence, KV head) split on its own;
-// one batch entry fills the SMs once, since its splits are equal, several have
-// lengths of their own, so their CTAs are cut to fill them about four times
-// over and the SMs even out.
-constexpr int TREE_FEW_ROWS = 64;
+// nodes, 64 keys, two CTAs per SM, each (sequence, KV head) split on its own:
+// so that the CTAs fill the SMs once, or, for several sequences, whose lengths
+// may differ, up to four times as long as a CTA keeps 1024 keys.
+constexpr int TREE_FEW_ROWS = 32;
 constexpr int TREE_SMS = 148;
 __host__ __device__ inline bool tree_few_rows(int T, int R) { return T * R <= TREE_FEW_ROWS; }
 inline int tree_key_tile(int T, int R) { return tree_few_rows(T, R) ? 128 : 64; }
@@ -138,9 +137,11 @@ inline int tree_splits(int B, int T, int Hkv, int R, int64_t capacity) {
     return static_cast<int>(tiles < TREE_SMS ? tiles : TREE_SMS);
   }
   const int tile = tree_tile_nodes(T, R), row_tiles = (T + tile - 1) / tile;
-  const int64_t want = (B == 1 ? 2 * TREE_SMS : 8 * TREE_SMS) / (units * row_tiles);
-  const int64_t most = (capacity + 255) / 256;
-  const int64_t n = want < most ? want : most;
+  const int64_t once = 2 * TREE_SMS / (units * row_tiles);
+  int64_t n = B == 1 ? 0 : 8 * TREE_SMS / (units * row_tiles);
+  if (n > capacity / 1024) n = capacity / 1024;
+  if (n < once) n = once;
+  if (n > (capacity + 255) / 256) n = (capacity + 255) / 256;
   return static_cast<int>(n < 1 ? 1 : n);
 }
 // The workspace: partial O, partial LSE, prefix sums, each from a multiple of 256.

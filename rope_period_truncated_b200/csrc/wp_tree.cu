@@ -452,6 +452,7 @@ constexpr int COMBINE_WARPS = 4;
 template <int D>
 __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int E = D / 32;
+  cudaGridDependencySynchronize();
   const int R = a.Hq / a.cache.Hkv;
   const int64_t id = static_cast<int64_t>(blockIdx.x) * COMBINE_WARPS + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -469,13 +470,26 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const 
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   const bool there = plan.ok && row / R < plan.n;
   if (there) {
-    for (int s = 0; s < splits; ++s) M = fmaxf(M, lp[s]);
-    spoilt = M == INFINITY;
-    for (int s = 0; s < splits; ++s) {
-      const float w = lp[s] == -INFINITY ? 0.f : fast_exp2(lp[s] - M);
-      sum += w;
+    for (int s = lane; s < splits; s += 32) M = fmaxf(M, lp[s]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += w * op[static_cast<int64_t>(s) * D + e];
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    spoilt = M == INFINITY;
+    for (int s = 0; s < splits; s += 4) {
+      float w[4], v[4][E];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at = min(s + k, splits - 1);
+        const float l = lp[at];
+        w[k] = s + k >= splits || l == -INFINITY ? 0.f : fast_exp2(l - M);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = op[static_cast<int64_t>(at) * D + e];
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum += w[k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += w[k] * v[k][e];
+      }
     }
   }
   __nv_bfloat16 *o = a.o + out_row(a, b, hk, R, row) * D + lane * E;
@@ -509,9 +523,17 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
 template <int D>
 cudaError_t combine(const TreeArgs &a, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
-  const unsigned blocks = static_cast<unsigned>((rows + COMBINE_WARPS - 1) / COMBINE_WARPS);
-  tree_combine_kernel<D><<<blocks, COMBINE_WARPS * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+  // started while the first kernel runs; it waits for its results on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + COMBINE_WARPS - 1) / COMBINE_WARPS));
+  cfg.blockDim = dim3(COMBINE_WARPS * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, a);
 }
 
 }  // namespace

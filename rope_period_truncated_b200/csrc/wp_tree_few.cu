@@ -11,15 +11,18 @@
 // One CTA per SM. All (sequence, KV head) units lie end to end as a line of
 // 128-key tiles, cut evenly among the CTAs, whatever the lengths: a CTA walks
 // over its stretch in segments (what of one unit falls into it), and its loads
-// run ahead across them. Warps 4 and 5 fetch K and V, warp 6 issues S^T (M =
-// 128 keys, N = rows, one K = 16 product per live group, two buffers in TMEM),
-// warps 0-3 turn it into P^T (bf16, in shared memory: B of the second product,
-// rows contiguous), warp 7 issues O^T (M = 128 dims, V read as it lies,
-// MN-major). A segment that is a whole unit writes its rows; the others, at
-// most the first and the last of a CTA, write O (fp32) and LSE to the
-// workspace, and a second kernel merges them.
+// run ahead across them. Warps 8 and 9 fetch K, and Q and V, warp 10 issues S^T
+// (M = 128 keys, N = rows, one K = 16 product per live group), warps 0-3 turn it
+// into P^T for the even tiles and warps 4-7 for the odd ones (bf16, in shared
+// memory: B of the second product, rows contiguous), warp 11 issues O^T (M = 128
+// dims, V read as it lies, MN-major). Even and odd tiles have maxima, sums and
+// an O^T of their own: a softmax warp alone on its scheduler waits for its own
+// latencies, about 1900 cycles a tile; two of them overlap. A segment that is a
+// whole unit writes its rows; the others, at most the first and the last of a
+// CTA, write O (fp32) and LSE to the workspace, and a second kernel merges
+// them.
 //
-// The running maxima are one per row for the whole CTA, kept in shared memory,
+// The running maxima are one per row and stream, kept in shared memory,
 // and stay as they are while no logit exceeds them by more than 2^8: a tile
 // then needs only one vote. Otherwise (the first tile, and rarely later) the
 // exact maxima are formed with warp reductions and O^T and the sums rescaled.
@@ -34,12 +37,14 @@ namespace wp {
 namespace {
 
 constexpr int TILE = 128;
+constexpr int FEW_THREADS = 384;
+constexpr int FEW_K_WARP = 8, FEW_V_WARP = 9, FEW_QK_WARP = 10, FEW_PV_WARP = 11;
 constexpr int SMEM_CAP = 232448;  // dynamic shared memory of one CTA
 constexpr uint32_t GROUP = TILE * 32;   // 128 keys x 16 bf16 (group-major K)
 constexpr uint32_t CHUNK = TILE * 128;  // 128 keys x 64 bf16 (K in rows)
 constexpr int PAGE_FLAGS = 16;  // of segments: V is loaded up to TREE_MAX_STAGES tiles ahead of the softmax
 constexpr int TABLES = 4;  // of segments in flight: S runs at most two tiles ahead of the softmax
-constexpr uint32_t NUM_BARS = 4 + 4 * TREE_MAX_STAGES + 4 * 2 + TABLES + 5;
+constexpr uint32_t NUM_BARS = 4 + 4 * TREE_MAX_STAGES + 4 * 2 + TABLES + 7;
 
 // The nodes of one segment's sequence.
 struct NodeTable {
@@ -59,8 +64,8 @@ struct FewLayout {
   static constexpr uint32_t P_TILE = TILE * NR * 2;
   static constexpr uint32_t Q_TILE = NR * 32;
   static constexpr uint32_t Q_BYTES = G * Q_TILE;
-  // node tables, scratch, and per row: -max, rescaling, 4 warps' values
-  static constexpr uint32_t SMALL = TABLES * sizeof(NodeTable) + 64 * 4 + NR * 4 * 6;
+  // node tables, scratch, and per row and stream: -max, a factor, 4 warps' values
+  static constexpr uint32_t SMALL = TABLES * sizeof(NodeTable) + 64 * 4 + 2 * NR * 4 * 6;
   static constexpr uint32_t FIXED = 2 * P_TILE + 2 * Q_BYTES + SMALL + NUM_BARS * 8 + 32 + PAGE_FLAGS * 4 + 1024;  // + alignment
   uint32_t v_off, p_off, q_off, small_off, bar_off, misc_off;
   __host__ __device__ FewLayout(int kst, int vst) {
@@ -131,14 +136,28 @@ struct Walk {
   }
 };
 
+// TMEM -> registers, 32 lanes x 32 bit, 16 consecutive columns, and the wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // TMEM columns [0, N) of this warp's lanes.
 template <int N>
 __device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[N]) {
   if constexpr (N == 64) {
     tmem_ld64(taddr, r);
-  } else {
+  } else if constexpr (N == 32) {
     tmem_ld32(taddr, r);
     tmem_wait_ld(r);
+  } else {
+    tmem_ld16(taddr, r);
   }
 }
 template <int N>
@@ -164,26 +183,27 @@ __device__ __forceinline__ int ordered(uint32_t x) {
 }
 
 template <int D, bool KGM, int NR>
-__global__ void __launch_bounds__(NTHREADS, 1)
+__global__ void __launch_bounds__(FEW_THREADS, 1)
     tree_few_kernel(const __grid_constant__ TreeMaps tm, const __grid_constant__ TreeArgs a) {
   using L = FewLayout<D, NR>;
   constexpr int G = D / 16;
   constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, NR, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, NR, true, true);
-  constexpr uint32_t TMEM_COLS = NR == 64 ? 256 : 128;  // S^T twice, O^T
+  constexpr uint32_t TMEM_COLS = 4 * NR;  // S^T and O^T of both streams
   constexpr uint32_t COL_O = 2 * NR;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const L lay(a.k_stages, a.v_stages);
   NodeTable *tables = reinterpret_cast<NodeTable *>(smem + lay.small_off);
   int32_t *jump = reinterpret_cast<int32_t *>(tables + TABLES);
-  float *negm = reinterpret_cast<float *>(jump + 64), *alpha = negm + NR;  // minus the running maxima; rescaling
-  float *part4 = alpha + NR;                                               // [4][NR] of the warps
+  float *all_negm = reinterpret_cast<float *>(jump + 64);  // [2][NR] minus the running maxima
+  float *all_alpha = all_negm + 2 * NR;                    // [2][NR] rescaling, at the end the streams' factors
+  float *all_part = all_alpha + 2 * NR;                    // [2][4][NR] of the warps
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.bar_off);
   uint64_t *q_full = bars, *q_empty = q_full + 2, *k_full = q_empty + 2, *k_empty = k_full + TREE_MAX_STAGES,
            *v_full = k_empty + TREE_MAX_STAGES, *v_empty = v_full + TREE_MAX_STAGES, *s_ready = v_empty + TREE_MAX_STAGES,
            *s_free = s_ready + 2, *p_ready = s_free + 2, *o_ready = p_ready + 2, *t_ready = o_ready + 2,
-           *o_final = t_ready + TABLES, *bnd_ready = o_final + 1, *bnd_done = bnd_ready + 1, *drain = bnd_done + 1;
+           *o_final = t_ready + TABLES, *bnd_ready = o_final + 1, *bnd_done = bnd_ready + 2, *drain = bnd_done + 2;
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + lay.misc_off);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lay.misc_off + 4);
   volatile int *bad_pages = reinterpret_cast<volatile int *>(smem + lay.misc_off + 32);  // set by the V producer
@@ -213,20 +233,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&s_free[s], 4);
       mbar_init(&p_ready[s], 4);
       mbar_init(&o_ready[s], 1);
+      mbar_init(&bnd_ready[s], 1);
+      mbar_init(&bnd_done[s], 4);
       mbar_init(&drain[s], 1);
     }
     mbar_init(o_final, 1);
-    mbar_init(bnd_ready, 1);
-    mbar_init(bnd_done, 4);
     fence_barrier_init();
   }
-  if (warp == QK_WARP) {
+  if (warp == FEW_QK_WARP) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
   }
   // rows of Q beyond the last one, as zeros (their columns of S^T take part in the votes)
   const int pad = (NR - rows) * 2;  // 16-byte pieces per group
-  for (int e = threadIdx.x; e < pad * G * 2; e += NTHREADS)
+  for (int e = threadIdx.x; e < pad * G * 2; e += FEW_THREADS)
     *reinterpret_cast<uint4 *>(smem + lay.q_off + (e / pad) * L::Q_TILE + rows * 32 + (e % pad) * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_async_shared();
 
@@ -234,22 +254,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   // them by a scan over the block. CTA 0 writes them down for the merge.
   Walk walk;
   {
-    const int run = (a.B + NTHREADS - 1) / NTHREADS, b0 = min(static_cast<int>(threadIdx.x) * run, a.B), b1 = min(b0 + run, a.B);
+    const int run = (a.B + FEW_THREADS - 1) / FEW_THREADS, b0 = min(static_cast<int>(threadIdx.x) * run, a.B), b1 = min(b0 + run, a.B);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += few_plan(a, b).tiles;
+    int own = 0;  // tiles of the last one
+    for (int b = b0; b < b1; ++b) mine += own = few_plan(a, b).tiles;
     int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(FULL, inc, o);
       if (lane >= o) inc += y;
     }
-    int64_t *sums = reinterpret_cast<int64_t *>(part4);  // 8 warps
+    int64_t *sums = reinterpret_cast<int64_t *>(all_part);  // of the warps
     if (lane == 31) sums[warp] = inc;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     int64_t before = inc - mine, total = 0;
-    for (int w = 0; w < NTHREADS / 32; ++w) {
+    #pragma unroll
+    for (int w = 0; w < FEW_THREADS / 32; ++w) {
       before += w < warp ? sums[w] : 0;
       total += sums[w];
     }
@@ -257,17 +279,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     walk.x = cut(tiles, blockIdx.x, gridDim.x);
     walk.x1 = cut(tiles, blockIdx.x + 1, gridDim.x);
     for (int b = b0; b < b1; ++b) {
-      const int t = few_plan(a, b).tiles;
+      const int t = run == 1 ? own : few_plan(a, b).tiles;
       if (blockIdx.x == 0 && a.prefix != nullptr) a.prefix[b] = before;
       const int64_t at = walk.x - before * cg.Hkv;  // the stretch's start within sequence b
       if (at >= 0 && at < static_cast<int64_t>(t) * cg.Hkv) {
         start[0] = b;
-        start[1] = static_cast<int>(at / t);
-        start[2] = static_cast<int>(at % t);
+        int h = 0;
+        int64_t rest = at;
+        for (; rest >= t; rest -= t) ++h;
+        start[1] = h;
+        start[2] = static_cast<int>(rest);
       }
       before += t;
     }
-    if (blockIdx.x == 0 && a.prefix != nullptr && threadIdx.x == NTHREADS - 1) a.prefix[a.B] = total;
+    if (blockIdx.x == 0 && a.prefix != nullptr && threadIdx.x == FEW_THREADS - 1) a.prefix[a.B] = total;
     __syncthreads();
     walk.cta = blockIdx.x;
     walk.index = 0;
@@ -283,26 +308,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int box = a.box_rows, boxes = TILE / box;
   Segment seg;
 
-  if (warp == K_WARP) {
-    // ---------------------------------------------------- producer of Q, K
+  if (warp == FEW_K_WARP) {
+    // ------------------------------------------------------- producer of K
     // One elected lane issues every copy, in a warp-uniform loop; lane i looks
     // up box i % boxes one tile ahead. A run of live groups goes in boxes of 4,
     // 2 and 1 groups where a tile is one box high (an issue costs about 100
     // cycles, whatever its size).
     const bool leader = elect_one();
     Ring ring;
-    int issued = 0, q_issued = 0;
+    int issued = 0;
     bool ok = true;
     while (ok && walk.next(a, seg)) {
-      const int qs = seg.index & 1;
-      if (seg.index >= 2 && !warp_wait_idle(&q_empty[qs], ((seg.index >> 1) - 1) & 1, lim, abort_flag)) break;
-      if (leader) {
-        mbar_arrive_expect_tx(&q_full[qs], G * 32u * rows);
-        for (int g = 0; g < G; ++g)
-          tma_load_4d(smem + lay.q_off + qs * L::Q_BYTES + g * L::Q_TILE, &tm.q, &q_full[qs], 16 * g, seg.hk * R, 0, seg.b);
-      }
-      __syncwarp();
-      ++q_issued;
       const int end = min(seg.k_begin + seg.tiles * TILE, seg.plan.total);
       const int key0 = seg.k_begin + (lane & (boxes - 1)) * box;
       Place here = place_of(cg, seg.b, key0, end);
@@ -339,26 +355,30 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     // no bulk copy may still be in flight when this CTA's shared memory goes
-    for (int s = 0; s < 2 && s < q_issued; ++s) {
-      const int last = s + ((q_issued - 1 - s) / 2) * 2;
-      warp_wait_idle(&q_full[s], (last / 2) & 1, lim, nullptr);
-    }
     for (int s = 0; s < a.k_stages && s < issued; ++s) {
       const int last = s + ((issued - 1 - s) / a.k_stages) * a.k_stages;
       warp_wait_idle(&k_full[s], (last / a.k_stages) & 1, lim, nullptr);
     }
-  } else if (warp == V_WARP) {
-    // ------------------------------------------------------- producer of V
+  } else if (warp == FEW_V_WARP) {
+    // -------------------------------------------------- producer of Q and V
     // It also looks at the pages: an entry outside the pool spoils the segment
     // (TMA reads nothing there and gives zeros).
     const bool leader = elect_one();
     Ring ring;
-    int issued = 0;
+    int issued = 0, q_issued = 0;
     bool ok = true;
     while (ok && walk.next(a, seg)) {
       const int end = min(seg.k_begin + seg.tiles * TILE, seg.plan.total);
       const int key0 = seg.k_begin + (lane & (boxes - 1)) * box;
       Place here = place_of(cg, seg.b, key0, end);
+      const int qs = seg.index & 1;
+      if (seg.index >= 2 && !warp_wait_idle(&q_empty[qs], ((seg.index >> 1) - 1) & 1, lim, abort_flag)) break;
+      if (leader) {
+        mbar_arrive_expect_tx(&q_full[qs], G * 32u * rows);
+        for (int g = 0; g < G; ++g)
+          tma_load_4d(smem + lay.q_off + qs * L::Q_BYTES + g * L::Q_TILE, &tm.q, &q_full[qs], 16 * g, seg.hk * R, 0, seg.b);
+      }
+      ++q_issued;
       if (leader) bad_pages[seg.index % PAGE_FLAGS] = 0;
       __syncwarp();
       for (int u = 0; u < seg.tiles; ++u) {
@@ -385,18 +405,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         here = next;
       }
     }
+    for (int s = 0; s < 2 && s < q_issued; ++s) {
+      const int last = s + ((q_issued - 1 - s) / 2) * 2;
+      warp_wait_idle(&q_full[s], (last / 2) & 1, lim, nullptr);
+    }
     for (int s = 0; s < a.v_stages && s < issued; ++s) {
       const int last = s + ((issued - 1 - s) / a.v_stages) * a.v_stages;
       warp_wait_idle(&v_full[s], (last / a.v_stages) & 1, lim, nullptr);
     }
-  } else if (warp == QK_WARP) {
+  } else if (warp == FEW_QK_WARP) {
     // ------------------------------------------------------- issuer of S^T
     const bool leader = elect_one();
     const uint64_t q_desc0 = smem_desc(smem_u32(smem + lay.q_off), 16, 256, SMEM_SWIZZLE_32B);
     const uint64_t k_desc = KGM ? smem_desc(smem_u32(smem), 16, 256, SMEM_SWIZZLE_32B)
                                 : smem_desc(smem_u32(smem), 16, 1024, SMEM_SWIZZLE_128B);
     Ring ring;
-    int bnd_cnt = 0, it = 0;  // it: tiles of all segments
+    int bnd_cnt[2] = {0, 0}, it = 0;  // it: tiles of all segments
     bool ok = true;
     while (ok && walk.next(a, seg)) {
       const int qs = seg.index & 1;
@@ -411,8 +435,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             acc = 1;
           }
       };
-      // The nodes' table. The softmax has taken S^T of two tiles ago, so it is
-      // at most two segments back, and this table's last reader is done.
+      // The nodes' table. Tile it - 2 has been taken by its softmax warps, and
+      // they are past tile it - 4 then; tile it - 3 belongs to the others. So
+      // three segments back is the oldest table in use.
       ok = it < 2 || warp_wait(&s_free[it & 1], ((it >> 1) - 1) & 1, lim, abort_flag);
       if (!ok) break;
       NodeTable &tab = tables[seg.index % TABLES];
@@ -455,13 +480,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           while (ok && next_boundary_class(a.cut, bnd, prev, &W, &groups)) {
             if (leader) {
               issue_groups(s_col, kst_desc, groups, acc);
-              umma_commit(bnd_ready);
+              umma_commit(&bnd_ready[hh]);
             }
             acc = 1;
             __syncwarp();
-            ok = warp_wait(bnd_done, bnd_cnt & 1, lim, abort_flag);
+            const int round = hh ? bnd_cnt[1]++ : bnd_cnt[0]++;
+            ok = warp_wait(&bnd_done[hh], round & 1, lim, abort_flag);
             tc_fence_after();
-            ++bnd_cnt;
             prev = W;
           }
           if (!ok) break;
@@ -480,7 +505,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     if (leader) umma_commit(&drain[0]);
     __syncwarp();
     warp_wait(&drain[0], 0, lim, nullptr);
-  } else if (warp == PV_WARP) {
+  } else if (warp == FEW_PV_WARP) {
     // ------------------------------------------------------- issuer of O^T
     const bool leader = elect_one();
     // A = V^T: dims contiguous (MN-major); 8-key row groups 1024 B and 64-dim
@@ -502,8 +527,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < TILE / 16; ++kk)
-            umma_ss(tmem + COL_O, vst_desc + v_step<D>(kk, box), pst_desc + kk * ((16 * NR * 2) >> 4), IDESC_PV,
-                    (u > 0 || kk > 0) ? 1u : 0u);
+            umma_ss(tmem + COL_O + NR * hh, vst_desc + v_step<D>(kk, box), pst_desc + kk * ((16 * NR * 2) >> 4), IDESC_PV,
+                    (u > 1 || kk > 0) ? 1u : 0u);  // each stream's first tile of the segment starts O^T
           umma_commit(&o_ready[hh]);
           umma_commit(&v_empty[ring.slot]);
           if (u == seg.tiles - 1) umma_commit(o_final);
@@ -519,9 +544,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // ------------------------------------------------------------- softmax
     // The four warps meet in a vote on every tile, so none leaves the loop by
     // itself: one whose wait gave up goes on to the vote and says so there.
-    const int kt = warp * 32 + lane;  // key of the tile == TMEM lane; head dim == lane of O^T
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const uint32_t o_addr = lane_addr + COL_O;
+    const int hh = warp / 4, w4 = warp % 4, st = threadIdx.x % 128;  // stream; warp and thread within it
+    const int kt = w4 * 32 + lane;  // key of the tile == TMEM lane; head dim == lane of O^T
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+    const uint32_t s_addr = lane_addr + NR * hh, o_addr = lane_addr + COL_O + NR * hh;
+    const int bar = 2 + hh;  // the stream's named barrier; 1: both streams
+    float *negm = all_negm + hh * NR, *alpha = all_alpha + hh * NR, *part4 = all_part + hh * 4 * NR;
     const float c2 = a.scale_log2;
     const uint64_t c2x2 = pack_f2(c2, c2);
     uint64_t l2[NR / 2];  // this thread's sums, two rows each
@@ -530,17 +558,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     Ring vr;  // the V stage of the tile
     while (walk.next(a, seg)) {
       const Plan &plan = seg.plan;
-      if (threadIdx.x < NR) negm[threadIdx.x] = -LOWEST;
+      if (st < NR) negm[st] = -LOWEST;
 #pragma unroll
       for (int i = 0; i < NR / 2; ++i) l2[i] = 0ull;
       const NodeTable &tab = tables[seg.index % TABLES];
       ok = ok && warp_wait(&t_ready[seg.index % TABLES], (seg.index / TABLES) & 1, lim, abort_flag);
-      named_sync(2, 128);
+      named_sync(bar, 128);
       const int deepest = tab.deepest;
+      bool fresh = true;  // no tile of this stream in the segment yet
       for (int u = 0; u < seg.tiles; ++u, ++it) {
-        const int hh = it & 1;
+        if ((it & 1) != hh) {
+          vr.next(a.v_stages);
+          continue;
+        }
         const int k0 = seg.k_begin + u * TILE, key = k0 + kt;
-        const uint32_t s_addr = lane_addr + NR * hh;
         const uint32_t cls = tile_classes<TILE>(my_cut, G, plan.len, deepest, k0, lane);
         const bool drafts = k0 + TILE > plan.len;
         const bool context = key < plan.len, there = key < plan.total;
@@ -553,103 +584,116 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // rows within the window: len + depth - kpos <= W
             const int64_t most = W + kpos - plan.len;
             const uint64_t keep = most < 0 ? 0ull : tab.upto[static_cast<int>(min(most, static_cast<int64_t>(deepest)))];
-            ok = warp_wait(bnd_ready, bnd_cnt & 1, lim, abort_flag);
+            ok = warp_wait(&bnd_ready[hh], bnd_cnt & 1, lim, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            uint32_t su[NR];
-            load_columns<NR>(s_addr, su);
-            keep_rows<NR>(su, keep, 0u);
-            store_columns<NR>(s_addr, su);
+#pragma unroll 1
+            for (int p = 0; p < NR; p += 32) {
+              uint32_t su[32];
+              load_columns<32>(s_addr + p, su);
+              keep_rows<32>(su, keep >> p, 0u);
+              store_columns<32>(s_addr + p, su);
+            }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bnd_done);
+            if (lane == 0) mbar_arrive(&bnd_done[hh]);
             ++bnd_cnt;
             prev = W;
           }
         }
         ok = ok && warp_wait(&s_ready[hh], (it >> 1) & 1, lim, abort_flag);
         tc_fence_after();
-        uint32_t su[NR];
-        if (cls == 0) {  // no product: zeros, by the same load
-#pragma unroll
-          for (int c = 0; c < NR; ++c) su[c] = 0u;
-          store_columns<NR>(s_addr, su);
-        }
-        load_columns<NR>(s_addr, su);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[hh]);
-        if (drafts) keep_rows<NR>(su, context ? ~0ull : there ? tab.seen_by[key - plan.len] : 0ull, 0xff800000u);
-        // Does any logit exceed its row's maximum by more than 2^8?
-        float over = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NR; c += 4) {
-          const float4 m4 = *reinterpret_cast<const float4 *>(negm + c);
-          float x0, x1, x2, x3;
-          unpack_f2(ffma2(pack_f2(__uint_as_float(su[c]), __uint_as_float(su[c + 1])), c2x2, pack_f2(m4.x, m4.y)), x0, x1);
-          unpack_f2(ffma2(pack_f2(__uint_as_float(su[c + 2]), __uint_as_float(su[c + 3])), c2x2, pack_f2(m4.z, m4.w)), x2, x3);
-          over = max3(over, max3(x0, x1, x2), x3);
-        }
-        if (named_any(2, 128, over > RESCALE_THRESHOLD || !ok)) {
-          if (named_any(2, 128, !ok)) {
-            ok = false;
-            break;
-          }
-          int *warp_max = reinterpret_cast<int *>(part4) + warp * NR;
-#pragma unroll
-          for (int c = 0; c < NR; ++c) {
-            const int mx = __reduce_max_sync(FULL, ordered(su[c]));
-            if (lane == (c & 31)) warp_max[c] = mx;
-          }
-          named_sync(2, 128);
-          if (threadIdx.x < NR) {
-            const int *p = reinterpret_cast<const int *>(part4) + threadIdx.x;
-            const int mx = max(max(p[0], p[NR]), max(p[2 * NR], p[3 * NR]));
-            const float m_old = -negm[threadIdx.x];
-            const float m_new = fmaxf(m_old, __int_as_float(ordered(static_cast<uint32_t>(mx))) * c2);
-            alpha[threadIdx.x] = fast_exp2(m_old - m_new);
-            negm[threadIdx.x] = -m_new;
-          }
-          named_sync(2, 128);
-          if (u > 0) {
-#pragma unroll
-            for (int c = 0; c < NR; c += 2) {
-              float l0, l1;
-              unpack_f2(l2[c / 2], l0, l1);
-              l2[c / 2] = pack_f2(l0 * alpha[c], l1 * alpha[c + 1]);
-            }
-            ok = warp_wait(&o_ready[hh ^ 1], ((it - 1) >> 1) & 1, lim, abort_flag);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c0 = 0; c0 < NR; c0 += 32) {
-              uint32_t ov[32];
-              tmem_ld32(o_addr + c0, ov);
-              tmem_wait_ld(ov);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha[c0 + c]);
-              tmem_st32(o_addr + c0, ov);
-            }
-            tmem_wait_st();
-          }
-        }
-        // P^T of two tiles ago must have been read before its place is written again
-        if (it >= 2) ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag) && ok;
+        const uint64_t visible = !drafts || context ? ~0ull : there ? tab.seen_by[key - plan.len] : 0ull;
         uint8_t *p_row = smem + lay.p_off + hh * L::P_TILE + kt * (NR * 2);
         const int turn = NR == 64 ? (kt & 7) : ((kt >> 1) & 3);  // the swizzle of the row's 16-byte pieces
+        bool gone = false;
 #pragma unroll
-        for (int c = 0; c < NR; c += 8) {
-          uint32_t w[4];
+        for (int part = 0; part < NR / 32; ++part) {  // 32 rows at a time, for the registers' sake
+          const int c0 = 32 * part;
+          uint32_t su[32];
+          if (cls == 0) {  // no product: zeros, by the same load
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint64_t m2 = *reinterpret_cast<const uint64_t *>(negm + c + 2 * e);
-            float x0, x1;
-            unpack_f2(ffma2(pack_f2(__uint_as_float(su[c + 2 * e]), __uint_as_float(su[c + 2 * e + 1])), c2x2, m2), x0, x1);
-            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-            l2[c / 2 + e] = fadd2(l2[c / 2 + e], pack_f2(p0, p1));
-            w[e] = pack_bf16x2(p0, p1);
+            for (int c = 0; c < 32; ++c) su[c] = 0u;
+            store_columns<32>(s_addr + c0, su);
           }
-          *reinterpret_cast<uint4 *>(p_row + (((c >> 3) ^ turn) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          load_columns<32>(s_addr + c0, su);
+          if (part == NR / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[hh]);
+          }
+          if (drafts) keep_rows<32>(su, visible >> c0, 0xff800000u);
+          // Does any logit exceed its row's maximum by more than 2^8?
+          float over = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 m4 = *reinterpret_cast<const float4 *>(negm + c0 + c);
+            float x0, x1, x2, x3;
+            unpack_f2(ffma2(pack_f2(__uint_as_float(su[c]), __uint_as_float(su[c + 1])), c2x2, pack_f2(m4.x, m4.y)), x0, x1);
+            unpack_f2(ffma2(pack_f2(__uint_as_float(su[c + 2]), __uint_as_float(su[c + 3])), c2x2, pack_f2(m4.z, m4.w)), x2, x3);
+            over = max3(over, max3(x0, x1, x2), x3);
+          }
+          if (named_any(bar, 128, over > RESCALE_THRESHOLD || !ok)) {
+            if (named_any(bar, 128, !ok)) {
+              gone = true;
+              break;
+            }
+            int *warp_max = reinterpret_cast<int *>(part4) + w4 * NR + c0;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int mx = __reduce_max_sync(FULL, ordered(su[c]));
+              if (lane == c) warp_max[c] = mx;
+            }
+            named_sync(bar, 128);
+            if (st < 32) {
+              const int r = c0 + st;
+              const int *p = reinterpret_cast<const int *>(part4) + r;
+              const int mx = max(max(p[0], p[NR]), max(p[2 * NR], p[3 * NR]));
+              const float m_old = -negm[r];
+              const float m_new = fmaxf(m_old, __int_as_float(ordered(static_cast<uint32_t>(mx))) * c2);
+              alpha[r] = fast_exp2(m_old - m_new);
+              negm[r] = -m_new;
+            }
+            named_sync(bar, 128);
+            if (!fresh) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                float l0, l1;
+                unpack_f2(l2[(c0 + c) / 2], l0, l1);
+                l2[(c0 + c) / 2] = pack_f2(l0 * alpha[c0 + c], l1 * alpha[c0 + c + 1]);
+              }
+              ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag);  // the stream's last P V
+              tc_fence_after();
+              uint32_t ov[32];
+              load_columns<32>(o_addr + c0, ov);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha[c0 + c]);
+              store_columns<32>(o_addr + c0, ov);
+            }
+          }
+          // P^T of two tiles ago must have been read before its place is written again
+          if (part == 0 && it >= 2) ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag) && ok;
+#pragma unroll
+          for (int c = c0; c < c0 + 32; c += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = c - c0 + 2 * e;
+              const uint64_t m2 = *reinterpret_cast<const uint64_t *>(negm + c + 2 * e);
+              float x0, x1;
+              unpack_f2(ffma2(pack_f2(__uint_as_float(su[i]), __uint_as_float(su[i + 1])), c2x2, m2), x0, x1);
+              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+              l2[c / 2 + e] = fadd2(l2[c / 2 + e], pack_f2(p0, p1));
+              w[e] = pack_bf16x2(p0, p1);
+            }
+            *reinterpret_cast<uint4 *>(p_row + (((c >> 3) ^ turn) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
+        if (gone) {
+          ok = false;
+          break;
+        }
+        fresh = false;
         if (u == seg.tiles - 1) {
           // The last tile: V has landed (so have the V producer's words on the
           // pages), and its rows behind the last key become zeros: unused slots
@@ -670,80 +714,83 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (ok && lane == 0) mbar_arrive(&p_ready[hh]);
       }
       // ---------------------------------------------------------- epilogue
+      // Both streams together: the sums of the rows over the four warps' keys,
+      // the factors that bring the two accumulators to one maximum, and half
+      // of the rows' results each.
       ok = ok && warp_wait(o_final, seg.index & 1, lim, abort_flag);
-      ok = !named_any(2, 128, !ok);  // all four warps or none
-      if (!ok) *abort_flag = 1;
-      const bool spoilt = !ok || tab.bad || bad_pages[seg.index % PAGE_FLAGS];
-      if (ok) {
-        // the rows' sums over the four warps' keys
 #pragma unroll
-        for (int c = 0; c < NR; c += 2) {
-          float l0, l1;
-          unpack_f2(l2[c / 2], l0, l1);
+      for (int c = 0; c < NR; c += 2) {
+        float l0, l1;
+        unpack_f2(l2[c / 2], l0, l1);
 #pragma unroll
-          for (int o = 16; o; o >>= 1) {
-            l0 += __shfl_xor_sync(FULL, l0, o);
-            l1 += __shfl_xor_sync(FULL, l1, o);
-          }
-          if (lane == 0) *reinterpret_cast<float2 *>(part4 + warp * NR + c) = make_float2(l0, l1);
+        for (int o = 16; o; o >>= 1) {
+          l0 += __shfl_xor_sync(FULL, l0, o);
+          l1 += __shfl_xor_sync(FULL, l1, o);
         }
-        tc_fence_after();
+        if (lane == 0) *reinterpret_cast<float2 *>(part4 + w4 * NR + c) = make_float2(l0, l1);
       }
-      named_sync(2, 128);
+      ok = !named_any(1, 256, !ok);  // all eight warps or none
+      if (!ok) *abort_flag = 1;
+      tc_fence_after();
+      const bool spoilt = !ok || tab.bad || bad_pages[seg.index % PAGE_FLAGS];
       if (threadIdx.x < rows) {
         const int r = threadIdx.x, node = r / R;
-        const float l = ok ? (part4[r] + part4[NR + r]) + (part4[2 * NR + r] + part4[3 * NR + r]) : 0.f;
-        const float m = -negm[r];
+        const auto sum4 = [&](const float *p) { return (p[r] + p[NR + r]) + (p[2 * NR + r] + p[3 * NR + r]); };
+        const float m0 = -all_negm[r], m1 = -all_negm[NR + r], m = fmaxf(m0, m1);
+        const float f0 = fast_exp2(m0 - m), f1 = fast_exp2(m1 - m);
+        const float l0 = sum4(all_part), l1 = sum4(all_part + 4 * NR), l = l0 * f0 + l1 * f1;
         const bool live = node < plan.n;
-        // rows of nodes that are not there are 0, a spoilt segment's NaN
-        alpha[r] = spoilt ? __int_as_float(0x7FC00000) : live && l != 0.f ? 1.f / l : 0.f;
+        // a stream without a visible key adds nothing, whatever its accumulator
+        // holds; rows of nodes that are not there are 0, a spoilt segment's NaN
+        const float inv = spoilt ? __int_as_float(0x7FC00000) : live && l != 0.f ? 1.f / l : 0.f;
+        all_alpha[r] = l0 == 0.f && !spoilt ? 0.f : f0 * inv;
+        all_alpha[NR + r] = l1 == 0.f && !spoilt ? 0.f : f1 * inv;
         if (seg.slot >= 0)
           a.lse_part[static_cast<int64_t>(seg.slot) * rows + r] = spoilt ? INFINITY : m + __log2f(l);
         else if (a.lse != nullptr)
           a.lse[(static_cast<int64_t>(seg.b) * a.Hq + seg.hk * R + r - node * R) * a.T + node] =
               spoilt ? __int_as_float(0x7FC00000) : live ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
       }
-      named_sync(2, 128);
-      // Lanes are head dims: 32 contiguous values of a row per warp. In the
-      // workspace the rows follow one another; in o a node's R heads do.
-      const int64_t base = seg.slot >= 0 ? static_cast<int64_t>(seg.slot) * rows * D
-                                         : (static_cast<int64_t>(seg.b) * a.T * a.Hq + seg.hk * R) * D;
-      const int64_t jump_node = static_cast<int64_t>(a.Hq - R) * D;  // beyond the R heads of a node
-      int64_t at = base + kt;
-      int head = 0;
-#pragma unroll 1
-      for (int c0 = 0; c0 < rows; c0 += 32) {
-        uint32_t ov[32];
-        tmem_ld32(o_addr + c0, ov);
-        tmem_wait_ld(ov);
-        if (kt < D) {
+      named_sync(1, 256);
+      // Lanes are head dims: 32 contiguous values of a row per warp.
+      constexpr int HALF = NR / 2;
+      uint32_t ov[2][HALF];
+      const uint32_t half_addr = lane_addr + COL_O + hh * HALF;
+      load_columns<HALF>(half_addr, ov[0]);
+      load_columns<HALF>(half_addr + NR, ov[1]);
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c0 + c < rows) {
-              const float f = alpha[c0 + c];
-              // a row that sees nothing is 0, whatever the accumulator holds
-              const float v = f == 0.f ? 0.f : __uint_as_float(ov[c]) * f;
-              if (seg.slot >= 0) {
-                a.o_part[at] = v;
-              } else {
-                a.o[at] = __float2bfloat16_rn(v);
-                if (++head == R) {
-                  head = 0;
-                  at += jump_node;
-                }
-              }
-              at += D;
+      for (int c = 0; c < HALF; ++c) {
+        const float f0 = all_alpha[hh * HALF + c], f1 = all_alpha[NR + hh * HALF + c];
+        ov[0][c] = __float_as_uint((f0 == 0.f ? 0.f : __uint_as_float(ov[0][c]) * f0) + (f1 == 0.f ? 0.f : __uint_as_float(ov[1][c]) * f1));
+      }
+      if (kt < D) {
+        const int r0 = hh * HALF;
+        if (seg.slot >= 0) {  // the rows follow one another
+          float *dst = a.o_part + (static_cast<int64_t>(seg.slot) * rows + r0) * D + kt;
+#pragma unroll
+          for (int c = 0; c < HALF; ++c)
+            if (r0 + c < rows) dst[c * D] = __uint_as_float(ov[0][c]);
+        } else {  // a node's R heads do
+          __nv_bfloat16 *dst = a.o + (static_cast<int64_t>(seg.b) * a.T * a.Hq + seg.hk * R) * D + kt;
+          int node = r0 / R, head = r0 - node * R;
+#pragma unroll
+          for (int c = 0; c < HALF; ++c) {
+            if (r0 + c < rows) dst[(static_cast<int64_t>(node) * a.Hq + head) * D] = __float2bfloat16_rn(__uint_as_float(ov[0][c]));
+            if (++head == R) {
+              head = 0;
+              ++node;
             }
+          }
         }
       }
       tc_fence_before();
-      named_sync(2, 128);  // part4, alpha and negm are free again
+      named_sync(1, 256);  // O^T, the sums and the factors are free again
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == QK_WARP) {
+  if (warp == FEW_QK_WARP) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
@@ -833,18 +880,13 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
   const int smem = static_cast<int>(L::FIXED + stages * L::STAGE);
   cudaError_t e = cudaFuncSetAttribute(tree_few_kernel<D, KGM, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  tree_few_kernel<D, KGM, NR><<<a.nsplit, NTHREADS, smem, stream>>>(tm, a);
+  tree_few_kernel<D, KGM, NR><<<a.nsplit, FEW_THREADS, smem, stream>>>(tm, a);
   return cudaGetLastError();
-}
-
-template <int D, bool KGM>
-cudaError_t launch_rows(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
-  return a.T * (a.Hq / a.cache.Hkv) <= 32 ? launch<D, KGM, 32>(tm, a, stream) : launch<D, KGM, 64>(tm, a, stream);
 }
 
 template <int D>
 cudaError_t launch_both(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
-  const cudaError_t e = a.cache.k_group_major ? launch_rows<D, true>(tm, a, stream) : launch_rows<D, false>(tm, a, stream);
+  const cudaError_t e = a.cache.k_group_major ? launch<D, true, TREE_FEW_ROWS>(tm, a, stream) : launch<D, false, TREE_FEW_ROWS>(tm, a, stream);
   if (e != cudaSuccess) return e;
   // started while the first kernel runs; it waits for its results on the device
   const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
