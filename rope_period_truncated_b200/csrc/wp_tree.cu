@@ -453,13 +453,11 @@ template <int D>
 __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int E = D / 32;
   cudaGridDependencySynchronize();
-  const int R = a.Hq / a.cache.Hkv;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * COMBINE_WARPS + threadIdx.x / 32;
+  const int R = a.Hq / a.cache.Hkv, rows = a.T * R;
+  const int row = static_cast<int>(blockIdx.x) * COMBINE_WARPS + static_cast<int>(threadIdx.x) / 32, hk = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x % 32;
-  if (id >= static_cast<int64_t>(a.B) * a.T * a.Hq) return;
-  const int row = static_cast<int>(id % (a.T * R));
-  const int hk = static_cast<int>(id / (a.T * R) % a.cache.Hkv);
-  const int b = static_cast<int>(id / (a.T * R) / a.cache.Hkv);
+  if (row >= rows) return;
+  const int64_t id = (static_cast<int64_t>(b) * a.cache.Hkv + hk) * rows + row;
   const Plan plan = sequence_plan<SUB>(a, b);
   const int splits = sequence_splits<SUB>(a, plan.tiles);
   const float *lp = a.lse_part + id * a.nsplit;
@@ -522,10 +520,9 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
 
 template <int D>
 cudaError_t combine(const TreeArgs &a, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
   // started while the first kernel runs; it waits for its results on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + COMBINE_WARPS - 1) / COMBINE_WARPS));
+  cfg.gridDim = dim3((a.T * (a.Hq / a.cache.Hkv) + COMBINE_WARPS - 1) / COMBINE_WARPS, a.cache.Hkv, a.B);
   cfg.blockDim = dim3(COMBINE_WARPS * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr;

@@ -142,17 +142,48 @@ struct Work {
   int first_row, nodes;               // first node of the CTA's rows; nodes of one Q box
 };
 
+// Copies of one tile's K that `need` names: groups (group-major K) or 64-dim
+// chunks (K in rows). One elected lane issues them; an issue costs about 100
+// cycles, whatever its size, so where a tile is one box high a run of groups
+// goes in boxes of 4, 2 and 1.
+template <int D, bool KGM, int TILE>
+__device__ __forceinline__ void issue_k(const TreeMaps &tm, const Place &here, int have, uint32_t need, int box, int hk,
+                                        uint8_t *dst, uint64_t *full, bool leader) {
+  constexpr uint32_t GROUP = TILE * 32, CHUNK = TILE * 128;
+  constexpr int PIECES = KGM ? D / 16 : D / 64;
+  if (box == TILE) {
+    const int page = __shfl_sync(FULL, here.page, 0), row = __shfl_sync(FULL, here.row, 0);
+    if (leader && have) {
+      for (uint32_t left = need; left;) {
+        const int g = __ffs(left) - 1;
+        const uint32_t run = left >> g;
+        const int wide = KGM && (run & 0xfu) == 0xfu ? 2 : (run & 3u) == 3u ? 1 : 0;  // log2 of the box
+        tma_load_5d(dst + g * (KGM ? GROUP : CHUNK), &tm.k[wide], full, 0, row, g, hk, page);
+        left &= ~(((1u << (1 << wide)) - 1) << g);
+      }
+    }
+  } else {
+    for (int i = 0; i < have; ++i) {  // the boxes that exist come first
+      const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
+      uint8_t *at = dst + i * box * (KGM ? 32 : 128);
+      if (leader) {
+#pragma unroll
+        for (int g = 0; g < PIECES; ++g)
+          if (need & (1u << g)) tma_load_5d(at + g * (KGM ? GROUP : CHUNK), &tm.k[0], full, 0, row, g, hk, page);
+      }
+    }
+  }
+  __syncwarp();
+}
+
 // Producer of Q and K. Lane i looks up box i % boxes one tile ahead of its
-// loads (a block table's entry arrives meanwhile); one elected lane issues
-// every copy, in a warp-uniform loop. A run of live groups goes in boxes of 4,
-// 2 and 1 groups where a tile is one box high: an issue costs about 100
-// cycles, whatever its size.
+// loads (a block table's entry arrives meanwhile).
 template <int D, bool KGM, int TILE>
 __device__ __forceinline__ void produce_k(const TreeMaps &tm, const TreeArgs &a, const Work &w, int len, uint8_t *q_smem,
                                           uint32_t q_tile, uint64_t *q_full, uint8_t *ring_smem, uint64_t *k_full,
                                           uint64_t *k_empty, volatile int *abort_flag) {
   constexpr int G = D / 16;
-  constexpr uint32_t GROUP = TILE * 32, CHUNK = TILE * 128, STAGE = TILE * D * 2;
+  constexpr uint32_t STAGE = TILE * D * 2;
   const CacheGeom &cg = a.cache;
   const int lane = threadIdx.x % 32, R = a.Hq / cg.Hkv;
   const int box = a.box_rows, boxes = TILE / box, stages = a.k_stages;
@@ -177,21 +208,7 @@ __device__ __forceinline__ void produce_k(const TreeMaps &tm, const TreeArgs &a,
     if (u >= stages && !warp_wait_idle(&k_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) break;
     const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
     if (leader) mbar_arrive_expect_tx(full, have * __popc(need) * box * (KGM ? 32u : 128u));
-    for (int i = 0; i < have; ++i) {  // the boxes that exist come first
-      const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
-      if (leader) {
-        uint32_t left = need;
-        while (left) {
-          const int g = __ffs(left) - 1;
-          const uint32_t run = left >> g;
-          const int wide = boxes > 1 ? 0 : KGM && (run & 0xfu) == 0xfu ? 2 : (run & 3u) == 3u ? 1 : 0;  // log2 of the box
-          tma_load_5d(dst + (KGM ? g * GROUP + i * box * 32 : g * CHUNK + i * box * 128), &tm.k[wide], full, 0, row, g, w.hk,
-                      page);
-          left &= ~(((1u << (1 << wide)) - 1) << g);
-        }
-      }
-      __syncwarp();
-    }
+    issue_k<D, KGM, TILE>(tm, here, have, need, box, w.hk, dst, full, leader);
     ++issued;
     ring.next(stages);
     here = next;
@@ -238,6 +255,21 @@ __device__ __forceinline__ void produce_v(const TreeMaps &tm, const TreeArgs &a,
     const int last = s + ((issued - 1 - s) / stages) * stages;
     warp_wait_idle(&v_full[s], (last / stages) & 1, lim, nullptr);
   }
+}
+
+// Lane i gets the sum over the warp of every lane's v[i]: at each step a lane
+// keeps half of its values and gives the other half away.
+__device__ __forceinline__ float warp_sums(float (&v)[32]) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(FULL, give, o);
+    }
+  return v[0];
 }
 
 // Offset, in 16-byte units, of 16 keys kk of a V tile from its start.

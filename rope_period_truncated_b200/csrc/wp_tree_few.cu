@@ -44,18 +44,17 @@ constexpr uint32_t GROUP = TILE * 32;   // 128 keys x 16 bf16 (group-major K)
 constexpr uint32_t CHUNK = TILE * 128;  // 128 keys x 64 bf16 (K in rows)
 constexpr int PAGE_FLAGS = 16;  // of segments: V is loaded up to TREE_MAX_STAGES tiles ahead of the softmax
 constexpr int TABLES = 4;  // of segments in flight: S runs at most two tiles ahead of the softmax
-constexpr uint32_t NUM_BARS = 4 + 4 * TREE_MAX_STAGES + 4 * 2 + TABLES + 7;
+constexpr uint32_t NUM_BARS = 2 + 4 * TREE_MAX_STAGES + 4 * 2 + TABLES + 7;
 
 // The nodes of one segment's sequence.
 struct NodeTable {
-  uint64_t sees[64];     // per node: the nodes it sees
   uint64_t seen_by[64];  // per node: the rows that see it
   uint64_t upto[64];     // per depth: the rows no deeper
   int32_t depth[64];
   int deepest, bad, pad[2];
 };
 
-// Shared memory: K ring, V ring, two P tiles, two Q (NR rows per group), then
+// Shared memory: K ring, V ring, two P tiles, Q (NR rows per group), then
 // the small tables and the barriers.
 template <int D, int NR>
 struct FewLayout {
@@ -65,14 +64,14 @@ struct FewLayout {
   static constexpr uint32_t Q_TILE = NR * 32;
   static constexpr uint32_t Q_BYTES = G * Q_TILE;
   // node tables, scratch, and per row and stream: -max, a factor, 4 warps' values
-  static constexpr uint32_t SMALL = TABLES * sizeof(NodeTable) + 64 * 4 + 2 * NR * 4 * 6;
-  static constexpr uint32_t FIXED = 2 * P_TILE + 2 * Q_BYTES + SMALL + NUM_BARS * 8 + 32 + PAGE_FLAGS * 4 + 1024;  // + alignment
+  static constexpr uint32_t SMALL = TABLES * sizeof(NodeTable) + 64 * 8 + 64 * 4 + 2 * NR * 4 * 6;
+  static constexpr uint32_t FIXED = 2 * P_TILE + Q_BYTES + SMALL + NUM_BARS * 8 + 32 + PAGE_FLAGS * 4 + 1024;  // + alignment
   uint32_t v_off, p_off, q_off, small_off, bar_off, misc_off;
   __host__ __device__ FewLayout(int kst, int vst) {
     v_off = kst * STAGE;
     p_off = v_off + vst * STAGE;
     q_off = p_off + 2 * P_TILE;
-    small_off = q_off + 2 * Q_BYTES;
+    small_off = q_off + Q_BYTES;
     bar_off = small_off + SMALL;
     misc_off = bar_off + NUM_BARS * 8;  // abort flag, TMEM base, start of the stretch; from 32: page flags
   }
@@ -81,16 +80,11 @@ struct FewLayout {
 // The line of tiles. Sequence b has plan.tiles tiles per KV head; prefix[b] is
 // the sum over the sequences before it. CTA c of G takes the tiles [cut(c),
 // cut(c + 1)).
-__device__ __forceinline__ int64_t cut(int64_t tiles, int c, int G) {
-  // tiles * c / G without leaving 64 bits: tiles < 2^16 x 2^16 x 2^23
-  return tiles / G * c + tiles % G * c / G;
-}
+// (fewer than 2^55 tiles: the products stay within 64 bits.)
+__device__ __forceinline__ int64_t cut(int64_t tiles, int c, int G) { return tiles * c / G; }
+// The CTA of tile x: the largest c with cut(c) <= x.
 __device__ __forceinline__ int cta_of(int64_t tiles, int64_t x, int G) {
-  int c = static_cast<int>(x / max(tiles / G, static_cast<int64_t>(1)));
-  c = min(c, G - 1);
-  while (c > 0 && cut(tiles, c, G) > x) --c;
-  while (cut(tiles, c + 1, G) <= x) ++c;
-  return c;
+  return static_cast<int>(((x + 1) * G - 1) / tiles);
 }
 
 // A sequence with no nodes has nothing to attend; one with bad lengths is left
@@ -195,12 +189,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const L lay(a.k_stages, a.v_stages);
   NodeTable *tables = reinterpret_cast<NodeTable *>(smem + lay.small_off);
-  int32_t *jump = reinterpret_cast<int32_t *>(tables + TABLES);
+  uint64_t *sees = reinterpret_cast<uint64_t *>(tables + TABLES);  // per node: the nodes it sees (scratch of the S^T issuer)
+  int32_t *jump = reinterpret_cast<int32_t *>(sees + 64);
   float *all_negm = reinterpret_cast<float *>(jump + 64);  // [2][NR] minus the running maxima
   float *all_alpha = all_negm + 2 * NR;                    // [2][NR] rescaling, at the end the streams' factors
   float *all_part = all_alpha + 2 * NR;                    // [2][4][NR] of the warps
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + lay.bar_off);
-  uint64_t *q_full = bars, *q_empty = q_full + 2, *k_full = q_empty + 2, *k_empty = k_full + TREE_MAX_STAGES,
+  uint64_t *q_full = bars, *q_empty = q_full + 1, *k_full = q_empty + 1, *k_empty = k_full + TREE_MAX_STAGES,
            *v_full = k_empty + TREE_MAX_STAGES, *v_empty = v_full + TREE_MAX_STAGES, *s_ready = v_empty + TREE_MAX_STAGES,
            *s_free = s_ready + 2, *p_ready = s_free + 2, *o_ready = p_ready + 2, *t_ready = o_ready + 2,
            *o_final = t_ready + TABLES, *bnd_ready = o_final + 1, *bnd_done = bnd_ready + 2, *drain = bnd_done + 2;
@@ -214,6 +209,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   const int R = a.Hq / cg.Hkv, rows = a.T * R;
   const long long lim = a.wait_limit;
   const int my_cut = lane < G ? a.cut[lane] : 0;
+  if (threadIdx.x == FEW_K_WARP * 32) {
+    tma_prefetch_desc(&tm.k[0]);
+    tma_prefetch_desc(&tm.k[1]);
+    tma_prefetch_desc(&tm.k[2]);
+    tma_prefetch_desc(&tm.v);
+    tma_prefetch_desc(&tm.q);
+  }
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -227,8 +229,6 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       mbar_init(&v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
       mbar_init(&s_ready[s], 1);
       mbar_init(&s_free[s], 4);
       mbar_init(&p_ready[s], 4);
@@ -237,6 +237,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       mbar_init(&bnd_done[s], 4);
       mbar_init(&drain[s], 1);
     }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(o_final, 1);
     fence_barrier_init();
   }
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   }
   // rows of Q beyond the last one, as zeros (their columns of S^T take part in the votes)
   const int pad = (NR - rows) * 2;  // 16-byte pieces per group
-  for (int e = threadIdx.x; e < pad * G * 2; e += FEW_THREADS)
+  for (int e = threadIdx.x; e < pad * G; e += FEW_THREADS)
     *reinterpret_cast<uint4 *>(smem + lay.q_off + (e / pad) * L::Q_TILE + rows * 32 + (e % pad) * 16) = make_uint4(0u, 0u, 0u, 0u);
   fence_async_shared();
 
@@ -310,10 +312,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 
   if (warp == FEW_K_WARP) {
     // ------------------------------------------------------- producer of K
-    // One elected lane issues every copy, in a warp-uniform loop; lane i looks
-    // up box i % boxes one tile ahead. A run of live groups goes in boxes of 4,
-    // 2 and 1 groups where a tile is one box high (an issue costs about 100
-    // cycles, whatever its size).
+    // Lane i looks up box i % boxes one tile ahead.
     const bool leader = elect_one();
     Ring ring;
     int issued = 0;
@@ -334,21 +333,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
         const int have = __popc(__ballot_sync(FULL, lane < boxes && key0 + u * TILE < end));
         if (leader) mbar_arrive_expect_tx(full, have * __popc(need) * box * (KGM ? 32u : 128u));
-        for (int i = 0; i < have; ++i) {
-          const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
-          if (leader) {
-            uint32_t left = need;
-            while (left) {
-              const int g = __ffs(left) - 1;
-              const uint32_t run = left >> g;
-              const int wide = boxes > 1 ? 0 : KGM && (run & 0xfu) == 0xfu ? 2 : (run & 3u) == 3u ? 1 : 0;  // log2 of the box
-              tma_load_5d(dst + (KGM ? g * GROUP + i * box * 32 : g * CHUNK + i * box * 128), &tm.k[wide], full, 0, row, g,
-                          seg.hk, page);
-              left &= ~(((1u << (1 << wide)) - 1) << g);
-            }
-          }
-          __syncwarp();
-        }
+        issue_k<D, KGM, TILE>(tm, here, have, need, box, seg.hk, dst, full, leader);
         ++issued;
         ring.next(a.k_stages);
         here = next;
@@ -371,12 +356,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       const int end = min(seg.k_begin + seg.tiles * TILE, seg.plan.total);
       const int key0 = seg.k_begin + (lane & (boxes - 1)) * box;
       Place here = place_of(cg, seg.b, key0, end);
-      const int qs = seg.index & 1;
-      if (seg.index >= 2 && !warp_wait_idle(&q_empty[qs], ((seg.index >> 1) - 1) & 1, lim, abort_flag)) break;
+      // one buffer: after the last S^T product of the segment before
+      if (seg.index >= 1 && !warp_wait_idle(q_empty, (seg.index - 1) & 1, lim, abort_flag)) break;
       if (leader) {
-        mbar_arrive_expect_tx(&q_full[qs], G * 32u * rows);
+        mbar_arrive_expect_tx(q_full, G * 32u * rows);
+#pragma unroll
         for (int g = 0; g < G; ++g)
-          tma_load_4d(smem + lay.q_off + qs * L::Q_BYTES + g * L::Q_TILE, &tm.q, &q_full[qs], 16 * g, seg.hk * R, 0, seg.b);
+          tma_load_4d(smem + lay.q_off + g * L::Q_TILE, &tm.q, q_full, 16 * g, seg.hk * R, 0, seg.b);
       }
       ++q_issued;
       if (leader) bad_pages[seg.index % PAGE_FLAGS] = 0;
@@ -405,10 +391,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         here = next;
       }
     }
-    for (int s = 0; s < 2 && s < q_issued; ++s) {
-      const int last = s + ((q_issued - 1 - s) / 2) * 2;
-      warp_wait_idle(&q_full[s], (last / 2) & 1, lim, nullptr);
-    }
+    if (q_issued > 0) warp_wait_idle(q_full, (q_issued - 1) & 1, lim, nullptr);
     for (int s = 0; s < a.v_stages && s < issued; ++s) {
       const int last = s + ((issued - 1 - s) / a.v_stages) * a.v_stages;
       warp_wait_idle(&v_full[s], (last / a.v_stages) & 1, lim, nullptr);
@@ -416,15 +399,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   } else if (warp == FEW_QK_WARP) {
     // ------------------------------------------------------- issuer of S^T
     const bool leader = elect_one();
-    const uint64_t q_desc0 = smem_desc(smem_u32(smem + lay.q_off), 16, 256, SMEM_SWIZZLE_32B);
+    const uint64_t q_desc = smem_desc(smem_u32(smem + lay.q_off), 16, 256, SMEM_SWIZZLE_32B);
     const uint64_t k_desc = KGM ? smem_desc(smem_u32(smem), 16, 256, SMEM_SWIZZLE_32B)
                                 : smem_desc(smem_u32(smem), 16, 1024, SMEM_SWIZZLE_128B);
     Ring ring;
     int bnd_cnt[2] = {0, 0}, it = 0;  // it: tiles of all segments
     bool ok = true;
     while (ok && walk.next(a, seg)) {
-      const int qs = seg.index & 1;
-      const uint64_t q_desc = q_desc0 + ((qs * L::Q_BYTES) >> 4);
       const auto issue_groups = [&](uint32_t s_col, uint64_t kst_desc, uint32_t groups, uint32_t acc) {
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -441,12 +422,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       ok = it < 2 || warp_wait(&s_free[it & 1], ((it >> 1) - 1) & 1, lim, abort_flag);
       if (!ok) break;
       NodeTable &tab = tables[seg.index % TABLES];
-      const bool bad = node_masks(a, seg.plan, seg.b, tab.sees, tab.depth, jump, &tab.deepest);
+      const bool bad = node_masks(a, seg.plan, seg.b, sees, tab.depth, jump, &tab.deepest);
       __syncwarp();
       const int deepest = tab.deepest;
       {
         const int r0 = lane, r1 = lane + 32;
-        const uint64_t m0 = r0 < rows ? tab.sees[r0 / R] : 0ull, m1 = r1 < rows ? tab.sees[r1 / R] : 0ull;
+        const uint64_t m0 = r0 < rows ? sees[r0 / R] : 0ull, m1 = r1 < rows ? sees[r1 / R] : 0ull;
         const int d0 = r0 < rows ? tab.depth[r0 / R] : 64, d1 = r1 < rows ? tab.depth[r1 / R] : 64;
         for (int u = 0; u < seg.plan.n; ++u) {
           const uint64_t lo = __ballot_sync(FULL, (m0 >> u) & 1), hi = __ballot_sync(FULL, (m1 >> u) & 1);
@@ -460,7 +441,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&t_ready[seg.index % TABLES]);
       }
-      ok = warp_wait(&q_full[qs], (seg.index >> 1) & 1, lim, abort_flag);
+      ok = warp_wait(q_full, seg.index & 1, lim, abort_flag);
       for (int u = 0; ok && u < seg.tiles; ++u, ++it) {
         const int hh = it & 1;
         const uint32_t cls = tile_classes<TILE>(my_cut, G, seg.plan.len, deepest, seg.k_begin + u * TILE, lane);
@@ -495,7 +476,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           issue_groups(s_col, kst_desc, cls & 0xffu, acc);
           umma_commit(&s_ready[hh]);
           umma_commit(&k_empty[ring.slot]);
-          if (u == seg.tiles - 1) umma_commit(&q_empty[qs]);
+          if (u == seg.tiles - 1) umma_commit(q_empty);
         }
         __syncwarp();
         ring.next(a.k_stages);
@@ -719,15 +700,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       // of the rows' results each.
       ok = ok && warp_wait(o_final, seg.index & 1, lim, abort_flag);
 #pragma unroll
-      for (int c = 0; c < NR; c += 2) {
-        float l0, l1;
-        unpack_f2(l2[c / 2], l0, l1);
+      for (int c0 = 0; c0 < NR; c0 += 32) {
+        float l[32];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          l0 += __shfl_xor_sync(FULL, l0, o);
-          l1 += __shfl_xor_sync(FULL, l1, o);
-        }
-        if (lane == 0) *reinterpret_cast<float2 *>(part4 + w4 * NR + c) = make_float2(l0, l1);
+        for (int c = 0; c < 32; c += 2) unpack_f2(l2[(c0 + c) / 2], l[c], l[c + 1]);
+        part4[w4 * NR + c0 + lane] = warp_sums(l);
       }
       ok = !named_any(1, 256, !ok);  // all eight warps or none
       if (!ok) *abort_flag = 1;
@@ -808,12 +785,9 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_few_merge_kernel(const 
   constexpr int E = D / 32;
   cudaGridDependencySynchronize();
   const int R = a.Hq / a.cache.Hkv, rows = a.T * R;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * MERGE_WARPS + threadIdx.x / 32;
+  const int row = static_cast<int>(blockIdx.x) * MERGE_WARPS + static_cast<int>(threadIdx.x) / 32, hk = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x % 32;
-  if (id >= static_cast<int64_t>(a.B) * a.cache.Hkv * rows) return;
-  const int row = static_cast<int>(id % rows);
-  const int64_t unit = id / rows;
-  const int hk = static_cast<int>(unit % a.cache.Hkv), b = static_cast<int>(unit / a.cache.Hkv);
+  if (row >= rows) return;
   const int64_t before = a.prefix[b], own = a.prefix[b + 1] - before, tiles = a.prefix[a.B] * a.cache.Hkv;
   float acc[E], sum = 1.f, M = 0.f;
   bool spoilt = false, live = false;
@@ -829,7 +803,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_few_merge_kernel(const 
     const int late = cut(tiles, c0, G) < x0 ? 1 : 0;
     const auto slot_of = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? late : 0)) * rows + row; };
     // with fewer tiles than CTAs some of them have none
-    const auto has = [&](int c) { return c <= c1 && cut(tiles, c, G) < cut(tiles, c + 1, G); };
+    const auto has = [&](int c) { return c <= c1 && (tiles >= G || cut(tiles, c, G) < cut(tiles, c + 1, G)); };
     live = row / R < (a.n_nodes != nullptr ? a.n_nodes[b] : a.T);
     M = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32)
@@ -889,9 +863,9 @@ cudaError_t launch_both(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stre
   const cudaError_t e = a.cache.k_group_major ? launch<D, true, TREE_FEW_ROWS>(tm, a, stream) : launch<D, false, TREE_FEW_ROWS>(tm, a, stream);
   if (e != cudaSuccess) return e;
   // started while the first kernel runs; it waits for its results on the device
-  const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.Hq;
+  const int rows = a.T * (a.Hq / a.cache.Hkv);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + MERGE_WARPS - 1) / MERGE_WARPS));
+  cfg.gridDim = dim3((rows + MERGE_WARPS - 1) / MERGE_WARPS, a.cache.Hkv, a.B);
   cfg.blockDim = dim3(MERGE_WARPS * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
