@@ -530,7 +530,7 @@ int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_row
 
 /* wp_decode_tree_workspace_bytes — size of the scratch that wp_decode_tree
  * needs; Lmax is the cache's capacity per sequence (paged: max_pages *
- * page_size). 0 on bad arguments. */
+ * page_size). 0 where it needs none, and on bad arguments. */
 size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, int Lmax);
 
 /*
@@ -555,8 +555,9 @@ size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, 
  *   group_cut    host [d_h/16], or NULL: dense.
  *   o            device bf16 out [B, T, H_q, d_h]; lse device fp32 out
  *                [B, H_q, T] (natural log, scale included), or NULL.
- *   workspace    device scratch, 256-byte aligned; contents on entry do not
- *                matter.
+ *   workspace    device scratch of at least wp_decode_tree_workspace_bytes(...)
+ *                bytes, 256-byte aligned (may be NULL where that is 0);
+ *                contents on entry do not matter.
  * A sequence whose length, node count, parents or pages are out of range gets
  * NaN rows (nothing is read through them). A wait that gives up records
  * WP_ERR_TIMEOUT (wp_device_status) and gives NaN rows.

@@ -5,10 +5,23 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
 namespace wp {
+
+// Lets `kernel` have `bytes` of dynamic shared memory, once per device.
+template <auto kernel>
+inline cudaError_t allow_shared_memory(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 // Defined beside the other calls' tensor maps and wait limit.
 long long wait_limit();
@@ -108,7 +121,8 @@ struct TreeArgs {
   __nv_bfloat16 *o;                         // [B, T, Hq, D]
   float *lse;                               // [B, Hq, T] or null
   float *o_part, *lse_part;                 // partial results, lse base 2
-  int64_t *prefix;                          // few rows: [B + 1] key tiles (per head) before each sequence
+  int64_t *prefix;                          // few rows: [B + 1] key tiles (per head) before each sequence,
+                                            // or null: a CTA per (sequence, KV head)
   int B, T, Hq;
   int tile_nodes, row_tiles;                // nodes per CTA, CTAs per KV head and split
   int nsplit, box_rows;                     // splits of the keys (few rows: CTAs); rows of one TMA box
@@ -121,17 +135,23 @@ struct TreeArgs {
 // How the work is cut. Up to 32 rows per KV head (R query heads of T nodes) go
 // to the kernel whose products have keys and dims as their 128 rows: tiles of
 // 128 keys, one CTA per SM, the tiles of all sequences and KV heads dealt out
-// evenly. More rows go to the one that has query rows there: tiles of whole
+// evenly; or, where no sequence can exceed 512 keys and the (sequence, KV head)
+// units are no more than the SMs, a CTA per unit, which needs no merge (its
+// launch and run cost 5 us, a tile about 1). More rows go to the one that has query rows there: tiles of whole
 // nodes, 64 keys, two CTAs per SM, each (sequence, KV head) split on its own:
 // so that the CTAs fill the SMs once, or, for several sequences, whose lengths
 // may differ, up to four times as long as a CTA keeps 1024 keys.
 constexpr int TREE_FEW_ROWS = 32;
 constexpr int TREE_SMS = 148;
 __host__ __device__ inline bool tree_few_rows(int T, int R) { return T * R <= TREE_FEW_ROWS; }
+inline bool tree_whole_units(int B, int T, int Hkv, int R, int64_t capacity) {
+  return tree_few_rows(T, R) && capacity <= 512 && static_cast<int64_t>(B) * Hkv <= TREE_SMS;
+}
 inline int tree_key_tile(int T, int R) { return tree_few_rows(T, R) ? 128 : 64; }
 inline int tree_tile_nodes(int T, int R) { return T < 128 / R ? T : 128 / R; }
 inline int tree_splits(int B, int T, int Hkv, int R, int64_t capacity) {
   const int64_t units = static_cast<int64_t>(B) * Hkv;
+  if (tree_whole_units(B, T, Hkv, R, capacity)) return static_cast<int>(units);
   if (tree_few_rows(T, R)) {
     const int64_t tiles = units * ((capacity + 127) / 128);
     return static_cast<int>(tiles < TREE_SMS ? tiles : TREE_SMS);
@@ -144,20 +164,22 @@ inline int tree_splits(int B, int T, int Hkv, int R, int64_t capacity) {
   if (n > (capacity + 255) / 256) n = (capacity + 255) / 256;
   return static_cast<int>(n < 1 ? 1 : n);
 }
-// The workspace: partial O, partial LSE, prefix sums, each from a multiple of 256.
+// The workspace: partial O, partial LSE, prefix sums, each from a multiple of
+// 256; nothing where nothing is merged.
 struct TreeWorkspace {
   size_t lse, prefix, bytes;  // offsets, and the whole
 };
 inline TreeWorkspace tree_workspace(int B, int T, int Hq, int Hkv, int D, int64_t capacity) {
   const int nsplit = tree_splits(B, T, Hkv, Hq / Hkv, capacity);
   const bool few = tree_few_rows(T, Hq / Hkv);
+  if (few ? tree_whole_units(B, T, Hkv, Hq / Hkv, capacity) : nsplit == 1) return TreeWorkspace{0, 0, 0};
   // few rows: two partial results per CTA, of the rows of one KV head
-  const size_t n = few ? static_cast<size_t>(nsplit) * 2 * T * (Hq / Hkv) : nsplit == 1 ? 0 : static_cast<size_t>(B) * T * Hq * nsplit;
+  const size_t n = few ? static_cast<size_t>(nsplit) * 2 * T * (Hq / Hkv) : static_cast<size_t>(B) * T * Hq * nsplit;
   const auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   TreeWorkspace w;
   w.lse = up(n * D * sizeof(float));
   w.prefix = w.lse + up(n * sizeof(float));
-  w.bytes = w.prefix + up(few ? (static_cast<size_t>(B) + 1) * sizeof(int64_t) : 1);
+  w.bytes = w.prefix + up(few ? (static_cast<size_t>(B) + 1) * sizeof(int64_t) : 0);
   return w;
 }
 

@@ -283,7 +283,7 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
                    int max_pages, int page_size, int n_pages, int B, int H_q, int H_kv, int d_h,
                    const int32_t *group_cut, float softmax_scale, void *o, float *lse, void *workspace,
                    size_t ws_bytes, void *stream) {
-  if (q == nullptr || lens == nullptr || parents == nullptr || o == nullptr || workspace == nullptr) return WP_ERR_ARG;
+  if (q == nullptr || lens == nullptr || parents == nullptr || o == nullptr) return WP_ERR_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(lens, 4) || !aligned(parents, 4) ||
       !aligned(n_nodes, 4) || !aligned(workspace, 256))
     return WP_ERR_ARG;
@@ -296,7 +296,8 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
   if (H_q % H_kv != 0 || !std::isfinite(softmax_scale)) return WP_ERR_ARG;
   if (T > TREE_MAX_NODES || H_q / H_kv > TREE_MAX_GROUP) return WP_ERR_UNSUPPORTED;
   const int64_t cap = cache_capacity(a.cache);
-  if (ws_bytes < wp_decode_tree_workspace_bytes(B, T, H_q, H_kv, d_h, static_cast<int>(cap))) return WP_ERR_ARG;
+  const TreeWorkspace w = tree_workspace(B, T, H_q, H_kv, d_h, cap);
+  if (w.bytes > 0 && (workspace == nullptr || ws_bytes < w.bytes)) return WP_ERR_ARG;
   for (int g = 0; g < 8; ++g) {
     a.cut[g] = (group_cut == nullptr || g >= d_h / 16) ? WP_CUTOFF_INF : group_cut[g];
     if (a.cut[g] < 0) return WP_ERR_ARG;
@@ -316,11 +317,10 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
   const int key_tile = tree_key_tile(T, R);
   a.box_rows = key_tile;  // of one box: never across a page, which holds a multiple of 16 keys
   while (block_table != nullptr && page_size % a.box_rows != 0) a.box_rows /= 2;
-  const TreeWorkspace w = tree_workspace(B, T, H_q, H_kv, D, cap);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.o_part = reinterpret_cast<float *>(ws);
   a.lse_part = reinterpret_cast<float *>(ws + w.lse);
-  a.prefix = reinterpret_cast<int64_t *>(ws + w.prefix);
+  a.prefix = w.bytes > 0 ? reinterpret_cast<int64_t *>(ws + w.prefix) : nullptr;
   a.wait_limit = wait_limit();
   const float scale = softmax_scale > 0.f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(double(d_h)));
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);

@@ -511,7 +511,7 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
   a.v_stages = stages / 2;
   a.k_stages = stages - a.v_stages;
   const int smem = static_cast<int>(Layout<D>(a.k_stages, a.v_stages, rows).bytes());
-  cudaError_t e = cudaFuncSetAttribute(tree_kernel<D, KGM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared_memory<tree_kernel<D, KGM>>(SMEM_PER_CTA);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.row_tiles * a.nsplit, a.cache.Hkv, a.B);
   tree_kernel<D, KGM><<<grid, NTHREADS, smem, stream>>>(tm, a);

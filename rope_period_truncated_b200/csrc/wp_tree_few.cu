@@ -255,7 +255,28 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
   // The line of tiles: each thread takes a run of sequences; the sums before
   // them by a scan over the block. CTA 0 writes them down for the merge.
   Walk walk;
-  {
+  walk.cta = blockIdx.x;
+  walk.index = 0;
+  walk.first = true;
+  if (a.prefix == nullptr) {
+    // a unit of its own
+    walk.b = blockIdx.x / cg.Hkv;
+    walk.hk = blockIdx.x - walk.b * cg.Hkv;
+    walk.t = 0;
+    walk.plan = few_plan(a, walk.b);
+    walk.x = 0;
+    walk.x1 = walk.plan.tiles;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (walk.x1 == 0)  // nothing to attend: zeros, or NaN where the lengths are bad
+      for (int e = threadIdx.x; e < rows * D; e += FEW_THREADS) {
+        const int r = e / D;
+        a.o[out_row(a, walk.b, walk.hk, R, r) * D + e % D] = __float2bfloat16_rn(walk.plan.ok ? 0.f : __int_as_float(0x7FC00000));
+        float *lse = out_lse(a, walk.b, walk.hk, R, r);
+        if (e % D == 0 && lse != nullptr) *lse = walk.plan.ok ? -INFINITY : __int_as_float(0x7FC00000);
+      }
+  } else {
     const int run = (a.B + FEW_THREADS - 1) / FEW_THREADS, b0 = min(static_cast<int>(threadIdx.x) * run, a.B), b1 = min(b0 + run, a.B);
     int64_t mine = 0;
     int own = 0;  // tiles of the last one
@@ -282,7 +303,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     walk.x1 = cut(tiles, blockIdx.x + 1, gridDim.x);
     for (int b = b0; b < b1; ++b) {
       const int t = run == 1 ? own : few_plan(a, b).tiles;
-      if (blockIdx.x == 0 && a.prefix != nullptr) a.prefix[b] = before;
+      if (blockIdx.x == 0) a.prefix[b] = before;
       const int64_t at = walk.x - before * cg.Hkv;  // the stretch's start within sequence b
       if (at >= 0 && at < static_cast<int64_t>(t) * cg.Hkv) {
         start[0] = b;
@@ -294,11 +315,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       }
       before += t;
     }
-    if (blockIdx.x == 0 && a.prefix != nullptr && threadIdx.x == FEW_THREADS - 1) a.prefix[a.B] = total;
+    if (blockIdx.x == 0 && threadIdx.x == FEW_THREADS - 1) a.prefix[a.B] = total;
     __syncthreads();
-    walk.cta = blockIdx.x;
-    walk.index = 0;
-    walk.first = true;
     if (walk.x < walk.x1) {
       walk.b = start[0];
       walk.hk = start[1];
@@ -852,7 +870,7 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
   a.v_stages = stages / 2;
   a.k_stages = stages - a.v_stages;
   const int smem = static_cast<int>(L::FIXED + stages * L::STAGE);
-  cudaError_t e = cudaFuncSetAttribute(tree_few_kernel<D, KGM, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_shared_memory<tree_few_kernel<D, KGM, NR>>(SMEM_CAP);
   if (e != cudaSuccess) return e;
   tree_few_kernel<D, KGM, NR><<<a.nsplit, FEW_THREADS, smem, stream>>>(tm, a);
   return cudaGetLastError();
@@ -861,7 +879,7 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_both(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
   const cudaError_t e = a.cache.k_group_major ? launch<D, true, TREE_FEW_ROWS>(tm, a, stream) : launch<D, false, TREE_FEW_ROWS>(tm, a, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.prefix == nullptr) return e;
   // started while the first kernel runs; it waits for its results on the device
   const int rows = a.T * (a.Hq / a.cache.Hkv);
   cudaLaunchConfig_t cfg = {};

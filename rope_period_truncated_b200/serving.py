@@ -368,7 +368,8 @@ def wp_decode_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, 
         lse = call.own(q.new_empty((B, Hq, T), dtype=F32))
     if workspace is None:
         ws = _load().wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d, Lmax if block_table is None else max_pages * page)
-        workspace = call.own(lens.new_empty(ws // 4))
+        if ws:
+            workspace = call.own(lens.new_empty(ws // 4))
     else:
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the same device")
@@ -376,7 +377,7 @@ def wp_decode_tree(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, 
     keep, cut = _cuts(group_cut, d // 16)
     call("wp_decode_tree", q.data_ptr(), kcache.data_ptr(), klay, vcache.data_ptr(), lens.data_ptr(), parents.data_ptr(), _ptr(n_nodes), T,
          Lmax, _ptr(block_table), max_pages, page, n_pages, B, Hq, Hkv, d, cut, softmax_scale, out.data_ptr(), _ptr(lse),
-         workspace.data_ptr(), ws)
+         _ptr(workspace), ws)
     return out, lse
 
 

@@ -190,12 +190,13 @@ def test_tree_bad_sequences_get_nan_rows():
 
 def test_tree_optional_arguments():
     """No node counts (all T), no LSE, given outputs and workspace; a workspace that is too small is refused."""
-    c = Case(41, 128, 4, 2, 6, [500, 20], [6, 6], 0, False)
+    c = Case(41, 128, 4, 2, 6, [1500, 20], [6, 6], 0, False)
     want, lse = c.run(ODD_CUT)
     o, none = wp.wp_decode_tree(*c.args(), group_cut=ODD_CUT, want_lse=False)
     assert none is None and torch.equal(o, want)
     need = wp.wp_decode_tree_workspace_bytes(2, 6, 4, 2, 128, c.v.shape[2])
     out, l2, ws = torch.empty_like(want), torch.empty_like(lse), torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    assert need > 0
     o, l = wp.wp_decode_tree(*c.args(), group_cut=ODD_CUT, out=out, lse=l2, workspace=ws)
     assert o is out and l is l2 and torch.equal(out, want) and torch.equal(l2, lse)
     with pytest.raises(wp.WavePruneError):

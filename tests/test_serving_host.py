@@ -144,7 +144,7 @@ def test_rope_append_rejects_bad_arguments(lib):
 # ------------------------------------------------------------------------ tree
 
 def test_decode_tree_rejects_bad_arguments(lib):
-    T, B, Hq, Hkv, d, Lmax = 8, 2, 8, 2, 128, 500
+    T, B, Hq, Hkv, d, Lmax = 8, 2, 8, 2, 128, 5000
     ws = lib.wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d, Lmax)
     cut = (ctypes.c_int32 * 8)(*([5] * 7 + [-1]))
     good = [FAKE, FAKE, 0, FAKE, FAKE, FAKE, None, T, Lmax, None, 0, 0, 0, B, Hq, Hkv, d, None, 0.0, FAKE, None, FAKE, ws, None]
@@ -160,6 +160,7 @@ def test_decode_tree_rejects_bad_arguments(lib):
         ({19: FAKE + 8}, ARG, "o misaligned"), ({20: FAKE + 2}, ARG, "lse misaligned"), ({21: None}, ARG, "workspace"),
         ({21: FAKE + 128}, ARG, "workspace misaligned"), ({22: ws - 1}, ARG, "workspace too small"),
         ({**paged, 11: 24}, ARG, "page size"), ({**paged, 12: 0}, ARG, "pool"), ({**paged, 10: 1 << 25}, UNSUPPORTED, "capacity")])
+    assert lib.wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d, 500) == 0  # short caches need none
     for change in ((0, 0), (1, 0), (1, 65), (2, 0), (3, 0), (4, 0), (5, 0)):
         args = [B, T, Hq, Hkv, d, Lmax]
         args[change[0]] = change[1]
