@@ -297,11 +297,15 @@ __global__ void __launch_bounds__(NTHREADS, 2)
           uint64_t keep = first <= 0 ? ~0ull : first >= 64 ? 0ull : ~0ull << first;
           if (drafts) {
             const int c0 = max(plan.len - k0, 0);  // first drafted column
-            if (c0 < 64) keep &= (1ull << c0) - 1;
+            const uint64_t drafted = ~0ull << c0;  // c0 < 64 here
+            keep &= ~drafted;
+            if (W >= deepest) {  // no two nodes are further apart
+              keep |= drafted;
+            } else {
+              const int c1 = min(plan.total - k0, 64);
 #pragma unroll 1
-            for (int c = c0; c < 64; ++c) {
-              const int node_c = k0 + c - plan.len;
-              if (node_c < 64 && pos - (plan.len + depth[node_c]) <= W) keep |= 1ull << c;
+              for (int c = c0; c < c1; ++c)
+                if (pos - (plan.len + depth[k0 + c - plan.len]) <= W) keep |= 1ull << c;
             }
           }
           ok = warp_wait(bnd_ready, bnd_cnt & 1, lim, abort_flag);
