@@ -49,7 +49,7 @@ typedef enum {
 /* RoPE rotation layouts. Interleaved [KC, RoPE matrix]: channel c rotates the
  * dim pair (2c, 2c+1). Half-split: channel c rotates (c, c + d_h/2), the
  * rotate_half convention of Llama/Qwen checkpoints.
- * WP_ROPE_HALF_SPLIT_PAIRED is for wp_rope_apply only: it rotates a half-split
+ * WP_ROPE_HALF_SPLIT_PAIRED is for the rotary calls only: it rotates a half-split
  * input exactly as WP_ROPE_HALF_SPLIT and writes channel c's pair to dims
  * (2c, 2c+1) of the output, i.e. in the interleaved order. Q.K^T is unchanged
  * when Q and K are permuted alike (V is untouched), so attention on paired Q

@@ -1,6 +1,7 @@
 """WavePrune causal attention for NVIDIA B200 (sm_100a).
 
-Thin ctypes binding of ``libwaveprune.so`` (C ABI in ``include/waveprune.h``).
+Thin binding of ``libwaveprune.so`` (C ABI in ``include/waveprune.h``): ctypes,
+and a compiled module for the serving calls, where microseconds count.
 Every function here only marshals arguments: tensors must already be
 contiguous, correctly typed and on the GPU; all arithmetic runs in the
 library's CUDA kernels (or, for the cutoff tables and tile schedule, in the
@@ -41,7 +42,7 @@ __all__ = [
 
 ROPE_INTERLEAVED = 0
 ROPE_HALF_SPLIT = 1
-ROPE_HALF_SPLIT_PAIRED = 2  # wp_rope_apply only: half-split rotation written in the interleaved order
+ROPE_HALF_SPLIT_PAIRED = 2  # rotary calls only: half-split rotation written in the interleaved order
 MODE_GROUPED = 0
 MODE_CHANNEL = 1
 CUTOFF_INF = 2 ** 31 - 1

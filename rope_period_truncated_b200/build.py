@@ -1,4 +1,6 @@
-"""Build libwaveprune.so in-tree with nvcc for sm_100a.
+"""Build libwaveprune.so in-tree with nvcc for sm_100a, and _calls.so, the
+compiled Python binding of the serving calls, with the C++ compiler against
+torch's headers.
 
 Usage: ``python -m rope_period_truncated_b200.build`` (or ``build()``).
 The library links the CUDA runtime statically and reaches the driver's
@@ -11,12 +13,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libwaveprune.so")
+BINDING = os.path.join(PKG, "_calls.so")
+BINDING_SOURCE = os.path.join(CSRC, "wp_torch.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -40,7 +45,27 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _build_binding(force: bool, verbose: bool) -> None:
+    deps = (BINDING_SOURCE, os.path.join(INCLUDE, "waveprune.h"))
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return
+    import torch
+    from torch.utils import cpp_extension
+    include = [f for p in cpp_extension.include_paths("cuda") for f in ("-isystem", p)]
+    libs = [f for p in cpp_extension.library_paths("cuda") for f in ("-L", p)]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], *include, BINDING_SOURCE, "-o", tmp, *libs,
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    _build_binding(force, verbose)
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
