@@ -558,6 +558,7 @@ size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, 
  *   workspace    device scratch of at least wp_decode_tree_workspace_bytes(...)
  *                bytes, 256-byte aligned (may be NULL where that is 0);
  *                contents on entry do not matter.
+ * o, lse and the workspace overlap nothing else.
  * A sequence whose length, node count, parents or pages are out of range gets
  * NaN rows (nothing is read through them). A wait that gives up records
  * WP_ERR_TIMEOUT (wp_device_status) and gives NaN rows.
@@ -581,6 +582,7 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
  *   lens_out     device int32 [B]; may be lens.
  *   cache        as in wp_rope_append. The pages written must not be shared
  *                with another sequence (wp_pages_update sees to it).
+ * lens_out, K and V overlap no other argument (but lens_out = lens).
  * A sequence with a bad length, path or page is left as it was, and its
  * lens_out is -1. A <= 1024. Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
  */
@@ -622,7 +624,8 @@ size_t wp_pages_update_workspace_bytes(int B, int n_pages);
  * range (WP_PAGES_BAD_ARGUMENT), nothing changes: the outputs are the inputs
  * and copies is empty. No output overlaps an input, another output or the
  * workspace (8-byte aligned; contents on entry do not matter).
- * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED (capacity above 2^30), WP_ERR_CUDA.
+ * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED (capacity or n_pages above 2^30, B
+ * above 65535), WP_ERR_CUDA.
  */
 int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32_t *lens, const int32_t *parent,
                     const int32_t *keep, const int32_t *new_lens, int32_t *refs_out, int32_t *block_table_out,
@@ -635,7 +638,8 @@ int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32
  * target page and the number of rows from the page's start, for every KV
  * head. An entry with a page outside the pool, rows outside 1..page_size, or
  * source = target copies nothing. A target page must not appear in another
- * entry. Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
+ * entry; the pools and copies do not overlap. Errors: WP_ERR_ARG,
+ * WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
  */
 int wp_pages_copy(void *k_pages, int k_layout, void *v_pages, const int32_t *copies, int n, int n_pages, int page_size,
                   int H_kv, int d_h, void *stream);

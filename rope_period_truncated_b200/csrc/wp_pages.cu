@@ -276,7 +276,8 @@ constexpr int COPY_THREADS = 256;
 __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const __grid_constant__ PagesCopyArgs a) {
   const CacheGeom &g = a.cache;
   const int i = blockIdx.x, h = blockIdx.y;
-  const int src = a.copies[3 * i], dst = a.copies[3 * i + 1], rows = a.copies[3 * i + 2];
+  const int32_t *c = a.copies + 3 * static_cast<int64_t>(i);
+  const int src = c[0], dst = c[1], rows = c[2];
   if (src < 0 || src >= g.n_pages || dst < 0 || dst >= g.n_pages || rows < 1 || rows > g.page_size || src == dst) return;
   const int per_row = g.D / 8;
   const int n = rows * per_row;
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const __grid_c
   const int b = blockIdx.x;
   const int len = a.lens[b], n = a.n_keep[b];
   if (threadIdx.x == 0) s_moves = 0;
-  bool bad = len < 0 || n < 0 || n > a.A;
+  bool bad = len < 0 || len > cache_capacity(g) || n < 0 || n > a.A;
   int first = INT_MAX;  // rows before it stay where they are
   for (int i = threadIdx.x; i < a.A; i += COMPACT_THREADS) {
     const int p = a.path[static_cast<int64_t>(b) * a.A + i];

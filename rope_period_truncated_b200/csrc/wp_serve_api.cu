@@ -116,6 +116,17 @@ int cache_args(void *kcache, int k_layout, void *vcache, int B, int Lmax, const 
   return WP_OK;
 }
 
+// Bytes of a K or V pool from its base.
+Extent pool_extent(const CacheGeom &g, const void *base) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(base);
+  return Extent{lo, lo + static_cast<uintptr_t>(g.n_pages) * g.Hkv * g.page_size * g.D * 2};
+}
+Extent extent(const void *p, size_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return Extent{lo, p == nullptr ? lo : lo + bytes};
+}
+bool meets(const Extent &x, const Extent &y) { return x.lo < y.hi && y.lo < x.hi; }
+
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? WP_OK : WP_ERR_CUDA; }
 
 bool layout_ok(int layout) {
@@ -179,7 +190,7 @@ int wp_rope_qk(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_rows *k
   if (!layout_ok(layout)) return WP_ERR_ARG;
   const int rc = head_dim_status(d_h);
   if (rc != WP_OK) return rc;
-  if (!rotary_args_ok(d_h, rot_dim, theta, freq_scale, scale_all) || !std::isfinite(amplitude)) return WP_ERR_ARG;
+  if (!rotary_args_ok(d_h, rot_dim, theta, freq_scale, scale_all) || !std::isfinite(static_cast<float>(amplitude))) return WP_ERR_ARG;
   if (!aligned(pos, 4)) return WP_ERR_ARG;
   if (H_q > 65535 || H_k > 65535 || static_cast<int64_t>(B) * N > 0x7fffffff) return WP_ERR_UNSUPPORTED;
   const bool paired = layout == WP_ROPE_HALF_SPLIT_PAIRED;
@@ -231,14 +242,11 @@ int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_row
   std::memset(&a, 0, sizeof(a));
   const int rc = cache_args(kcache, k_layout, vcache, B, Lmax, block_table, max_pages, page_size, n_pages, H_kv, d_h, &a.cache);
   if (rc != WP_OK) return rc;
-  if (!rotary_args_ok(d_h, rot_dim, theta, freq_scale, scale_all) || !std::isfinite(amplitude)) return WP_ERR_ARG;
+  if (!rotary_args_ok(d_h, rot_dim, theta, freq_scale, scale_all) || !std::isfinite(static_cast<float>(amplitude))) return WP_ERR_ARG;
   if (H_q > 65535) return WP_ERR_UNSUPPORTED;
   Extent ek, ev, eq, eo;
   if (!rows_ok(k, 1, T, H_kv, d_h, false, &ek) || !rows_ok(v, 1, T, H_kv, d_h, false, &ev)) return WP_ERR_ARG;
-  const uintptr_t pool = static_cast<uintptr_t>(a.cache.n_pages) * H_kv * a.cache.page_size * d_h * 2;
-  const Extent cache[2] = {{reinterpret_cast<uintptr_t>(kcache), reinterpret_cast<uintptr_t>(kcache) + pool},
-                           {reinterpret_cast<uintptr_t>(vcache), reinterpret_cast<uintptr_t>(vcache) + pool}};
-  const auto meets = [](const Extent &x, const Extent &y) { return x.lo < y.hi && y.lo < x.hi; };
+  const Extent cache[2] = {pool_extent(a.cache, kcache), pool_extent(a.cache, vcache)};
   if (meets(cache[0], cache[1])) return WP_ERR_ARG;
   for (const Extent &c : cache)
     if (meets(ek, c) || meets(ev, c)) return WP_ERR_ARG;
@@ -302,6 +310,14 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
     a.cut[g] = (group_cut == nullptr || g >= d_h / 16) ? WP_CUTOFF_INF : group_cut[g];
     if (a.cut[g] < 0) return WP_ERR_ARG;
   }
+  // the outputs and the workspace are written while the inputs are still read
+  const size_t nq = static_cast<size_t>(B) * T * H_q, nb = static_cast<size_t>(B) * 4;
+  const Extent parts[] = {extent(q, nq * d_h * 2),    extent(lens, nb),       extent(parents, nb * T), extent(n_nodes, nb),
+                          pool_extent(a.cache, kcache), pool_extent(a.cache, vcache), extent(block_table, nb * max_pages),
+                          extent(o, nq * d_h * 2),    extent(lse, nq * 4),    extent(w.bytes > 0 ? workspace : nullptr, w.bytes)};
+  for (int out = 7; out < 10; ++out)
+    for (int i = 0; i < out; ++i)
+      if (meets(parts[out], parts[i])) return WP_ERR_ARG;
   const int R = H_q / H_kv, D = d_h;
   a.lens = lens;
   a.parents = parents;
@@ -324,6 +340,7 @@ int wp_decode_tree(const void *q, const void *kcache, int k_layout, const void *
   a.wait_limit = wait_limit();
   const float scale = softmax_scale > 0.f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(double(d_h)));
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2e);
+  if (!std::isfinite(a.scale_log2)) return WP_ERR_ARG;
   // Q [B, T, Hq, D]; V and K in rows [pages, Hkv, P, D] with the dims as
   // chunks of 64; group-major K [pages, Hkv, G, P, 16]. K is promoted in L2 no
   // further than a line: its neighbours in memory may be out of window.
@@ -359,6 +376,13 @@ int wp_kv_compact(void *kcache, int k_layout, void *vcache, const int32_t *lens,
   const int rc = cache_args(kcache, k_layout, vcache, B, Lmax, block_table, max_pages, page_size, n_pages, H_kv, d_h, &a.cache);
   if (rc != WP_OK) return rc;
   if (A > COMPACT_MAX_PATH) return WP_ERR_UNSUPPORTED;
+  // sequences run side by side: what one of them writes, none may read
+  const size_t nb = static_cast<size_t>(B) * 4;
+  const Extent parts[] = {extent(path, nb * A), extent(n_keep, nb), extent(block_table, nb * max_pages), extent(lens, nb),
+                          extent(lens_out, nb), pool_extent(a.cache, kcache), pool_extent(a.cache, vcache)};
+  for (int out = 4; out < 7; ++out)
+    for (int i = 0; i < out; ++i)
+      if (meets(parts[out], parts[i]) && !(out == 4 && i == 3 && lens_out == lens)) return WP_ERR_ARG;
   a.lens = lens;
   a.path = path;
   a.n_keep = n_keep;
@@ -380,7 +404,7 @@ int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32
   for (const void *p : ptrs)
     if (p == nullptr || !aligned(p, p == workspace ? 8 : 4)) return WP_ERR_ARG;
   if (B <= 0 || max_pages <= 0 || page_size < 16 || page_size % 16 != 0 || n_pages <= 0) return WP_ERR_ARG;
-  if (static_cast<int64_t>(max_pages) * page_size > (1ll << 30)) return WP_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_pages) * page_size > (1ll << 30) || B > 65535 || n_pages > (1 << 30)) return WP_ERR_UNSUPPORTED;
   if (ws_bytes < wp_pages_update_workspace_bytes(B, n_pages)) return WP_ERR_ARG;
   // the outputs are written while the inputs are still read
   const size_t nb = static_cast<size_t>(B) * 4, nt = nb * max_pages, np = static_cast<size_t>(n_pages) * 4;
@@ -422,6 +446,8 @@ int wp_pages_copy(void *k_pages, int k_layout, void *v_pages, const int32_t *cop
   // any non-null block table: the pools are paged, the copies name their pages
   const int rc = cache_args(k_pages, k_layout, v_pages, 1, 0, copies, 1, page_size, n_pages, H_kv, d_h, &a.cache);
   if (rc != WP_OK) return rc;
+  const Extent k = pool_extent(a.cache, k_pages), v = pool_extent(a.cache, v_pages), c = extent(copies, static_cast<size_t>(n) * 12);
+  if (meets(k, v) || meets(k, c) || meets(v, c)) return WP_ERR_ARG;
   a.copies = copies;
   a.n = n;
   return from_cuda(launch_pages_copy(a, static_cast<cudaStream_t>(stream)));

@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     // every product must have finished before TMEM is given back
     if (leader) umma_commit(&drain[0]);
     __syncwarp();
-    warp_wait(&drain[0], 0, lim, nullptr);
+    warp_wait(&drain[0], 0, drain_limit(a), nullptr);
   } else if (warp == PV_WARP) {
     // --------------------------------------------------------- issuer of O
     const bool leader = elect_one();
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     }
     if (leader) umma_commit(&drain[1]);
     __syncwarp();
-    warp_wait(&drain[1], 0, lim, nullptr);
+    warp_wait(&drain[1], 0, drain_limit(a), nullptr);
   } else if (warp >= warp0 && warp < warp0 + warps) {
     // ------------------------------------------------------------- softmax
     const int r = (warp - warp0) * 32 + lane;  // row of the tile, in TMEM lane 32 * warp + lane

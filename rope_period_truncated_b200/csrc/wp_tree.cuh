@@ -20,6 +20,12 @@ constexpr int NTHREADS = 256;
 constexpr int K_WARP = 4, V_WARP = 5, QK_WARP = 6, PV_WARP = 7;
 constexpr float LOWEST = -3.4028234663852886e38f;  // of a running maximum: finite, so that m - m is 0
 
+// Cycles to wait for the CTA's own copies and products before it gives back its
+// shared memory and TMEM: they end by themselves, and a caller's short wait
+// limit must not let the CTA go before them.
+constexpr long long DRAIN_LIMIT = 2000000000;
+__device__ __forceinline__ long long drain_limit(const TreeArgs &a) { return max(a.wait_limit, DRAIN_LIMIT); }
+
 // Position in a ring of stages: slot, and the parity of its current round.
 struct Ring {
   int slot = 0;
@@ -214,10 +220,10 @@ __device__ __forceinline__ void produce_k(const TreeMaps &tm, const TreeArgs &a,
     here = next;
   }
   // no bulk copy may still be in flight when this CTA's shared memory goes
-  if (w.ntiles > 0) warp_wait_idle(q_full, 0, lim, nullptr);
+  if (w.ntiles > 0) warp_wait_idle(q_full, 0, drain_limit(a), nullptr);
   for (int s = 0; s < stages && s < issued; ++s) {
     const int last = s + ((issued - 1 - s) / stages) * stages;
-    warp_wait_idle(&k_full[s], (last / stages) & 1, lim, nullptr);
+    warp_wait_idle(&k_full[s], (last / stages) & 1, drain_limit(a), nullptr);
   }
 }
 
@@ -253,7 +259,7 @@ __device__ __forceinline__ void produce_v(const TreeMaps &tm, const TreeArgs &a,
   }
   for (int s = 0; s < stages && s < issued; ++s) {
     const int last = s + ((issued - 1 - s) / stages) * stages;
-    warp_wait_idle(&v_full[s], (last / stages) & 1, lim, nullptr);
+    warp_wait_idle(&v_full[s], (last / stages) & 1, drain_limit(a), nullptr);
   }
 }
 

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     // no bulk copy may still be in flight when this CTA's shared memory goes
     for (int s = 0; s < a.k_stages && s < issued; ++s) {
       const int last = s + ((issued - 1 - s) / a.k_stages) * a.k_stages;
-      warp_wait_idle(&k_full[s], (last / a.k_stages) & 1, lim, nullptr);
+      warp_wait_idle(&k_full[s], (last / a.k_stages) & 1, drain_limit(a), nullptr);
     }
   } else if (warp == FEW_V_WARP) {
     // -------------------------------------------------- producer of Q and V
@@ -409,10 +409,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         here = next;
       }
     }
-    if (q_issued > 0) warp_wait_idle(q_full, (q_issued - 1) & 1, lim, nullptr);
+    if (q_issued > 0) warp_wait_idle(q_full, (q_issued - 1) & 1, drain_limit(a), nullptr);
     for (int s = 0; s < a.v_stages && s < issued; ++s) {
       const int last = s + ((issued - 1 - s) / a.v_stages) * a.v_stages;
-      warp_wait_idle(&v_full[s], (last / a.v_stages) & 1, lim, nullptr);
+      warp_wait_idle(&v_full[s], (last / a.v_stages) & 1, drain_limit(a), nullptr);
     }
   } else if (warp == FEW_QK_WARP) {
     // ------------------------------------------------------- issuer of S^T
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     // every product must have finished before TMEM is given back
     if (leader) umma_commit(&drain[0]);
     __syncwarp();
-    warp_wait(&drain[0], 0, lim, nullptr);
+    warp_wait(&drain[0], 0, drain_limit(a), nullptr);
   } else if (warp == FEW_PV_WARP) {
     // ------------------------------------------------------- issuer of O^T
     const bool leader = elect_one();
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     }
     if (leader) umma_commit(&drain[1]);
     __syncwarp();
-    warp_wait(&drain[1], 0, lim, nullptr);
+    warp_wait(&drain[1], 0, drain_limit(a), nullptr);
   } else {
     // ------------------------------------------------------------- softmax
     // The four warps meet in a vote on every tile, so none leaves the loop by

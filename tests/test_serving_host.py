@@ -221,3 +221,41 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu():
         wp.wp_pages_update(i, i, i, i, i, i, 16)
     with pytest.raises(TypeError):
         wp.wp_pages_copy(x, x, i)
+
+
+# --------------------------------------------------------- arguments that meet
+
+def test_outputs_that_meet_other_arguments_are_refused(lib):
+    """What one block writes while another still reads it."""
+    M = 1 << 24
+    at = [FAKE + i * M for i in range(12)]
+    B, T, Hq, Hkv, d, Lmax, A = 2, 8, 8, 2, 128, 5000, 8
+    q, kc, vc, lens, parents, nodes, o, lse, ws = at[:9]
+    need = lib.wp_decode_tree_workspace_bytes(B, T, Hq, Hkv, d, Lmax)
+    tree = [q, kc, 0, vc, lens, parents, nodes, T, Lmax, None, 0, 0, 0, B, Hq, Hkv, d, None, 0.0, o, lse, ws, need, None]
+    oq, cache = B * T * Hq * d * 2, B * Hkv * Lmax * d * 2
+    _expect(lib.wp_decode_tree, tree, [
+        ({19: q}, ARG, "o over q"), ({19: q + oq - 16}, ARG, "o into q's end"), ({19: vc + cache - 16}, ARG, "o in V"), ({20: lens}, ARG, "lse over lens"),
+        ({20: o + oq - 4}, ARG, "lse in o"), ({21: kc}, ARG, "workspace in K"), ({21: parents}, ARG, "workspace over parents"),
+        ({21: lse}, ARG, "workspace over lse"), ({20: nodes}, ARG, "lse over the node counts"),
+        ({9: at[9], 10: 4, 11: 64, 12: 9, 20: at[9] + 28}, ARG, "lse over the block table"), ({18: 3e38}, ARG, "a scale beyond 32 bits")])
+    path, keep, out = at[4], at[5], at[6]
+    compact = [kc, 0, vc, lens, path, A, keep, out, 100, None, 0, 0, 0, B, Hkv, d, None]
+    _expect(lib.wp_kv_compact, compact, [
+        ({7: path + 4 * A}, ARG, "lens_out in path"), ({7: keep}, ARG, "lens_out over n_keep"), ({7: lens + 4}, ARG, "lens_out beside lens"),
+        ({2: kc}, ARG, "K and V in one pool"), ({2: kc + 16}, ARG, "K and V overlap"), ({3: kc}, ARG, "lens in K")])
+    _expect(lib.wp_pages_copy, [kc, 0, vc, lens, 4, 100, 16, Hkv, d, None], [({2: kc}, ARG, "K and V in one pool"), ({3: vc + 64}, ARG, "copies in V")])
+    if not torch.cuda.is_available():  # as far as the launch, which has no GPU here
+        assert lib.wp_kv_compact(*(compact[:7] + [lens] + compact[8:])) == wp.WP_ERR_CUDA
+
+
+def test_limits_of_the_page_transaction(lib):
+    M = 1 << 40
+    at = [FAKE + i * M for i in range(12)]
+    for B, n in ((65536, 100), (4, (1 << 30) + 1)):
+        assert lib.wp_pages_update(*at[:11], B, 10, 16, n, at[11], lib.wp_pages_update_workspace_bytes(B, n), None) == UNSUPPORTED
+
+
+def test_an_amplitude_beyond_32_bits_is_refused(lib):
+    q, qo = rows(FAKE, 256, 128, 64), rows(FAKE + (1 << 20), 256, 128, 64)
+    assert lib.wp_rope_qk(q, qo, 2, None, None, 0, 1, 2, 64, 64, None, 0, 1e4, None, 1.0, 1e39, 0, 0, None) == ARG
