@@ -137,10 +137,12 @@ struct TreeArgs {
 // 128 keys, one CTA per SM, the tiles of all sequences and KV heads dealt out
 // evenly; or, where no sequence can exceed 512 keys and the (sequence, KV head)
 // units are no more than the SMs, a CTA per unit, which needs no merge (its
-// launch and run cost 5 us, a tile about 1). More rows go to the one that has query rows there: tiles of whole
-// nodes, 64 keys, two CTAs per SM, each (sequence, KV head) split on its own:
-// so that the CTAs fill the SMs once, or, for several sequences, whose lengths
-// may differ, up to four times as long as a CTA keeps 1024 keys.
+// launch and run cost 5 us, a tile about 1). More rows go to the one that has
+// query rows there: tiles of whole nodes, 64 keys, two CTAs per SM, each
+// (sequence, KV head) split on its own: so that the CTAs fill the SMs once (256
+// of 296 places: 4 x 2.5K to 4K keys 30.7 us with 9 splits, 28.4 with 8), or,
+// for several sequences, whose lengths may differ, up to twice as long as a CTA
+// keeps 1024 keys (16 x 16K to 32K keys, 64 rows: 248 us, 261 with twice as many).
 constexpr int TREE_FEW_ROWS = 32;
 constexpr int TREE_SMS = 148;
 __host__ __device__ inline bool tree_few_rows(int T, int R) { return T * R <= TREE_FEW_ROWS; }
@@ -157,8 +159,8 @@ inline int tree_splits(int B, int T, int Hkv, int R, int64_t capacity) {
     return static_cast<int>(tiles < TREE_SMS ? tiles : TREE_SMS);
   }
   const int tile = tree_tile_nodes(T, R), row_tiles = (T + tile - 1) / tile;
-  const int64_t once = 2 * TREE_SMS / (units * row_tiles);
-  int64_t n = B == 1 ? 0 : 8 * TREE_SMS / (units * row_tiles);
+  const int64_t once = 256 / (units * row_tiles);
+  int64_t n = B == 1 ? 0 : 4 * TREE_SMS / (units * row_tiles);
   if (n > capacity / 1024) n = capacity / 1024;
   if (n < once) n = once;
   if (n > (capacity + 255) / 256) n = (capacity + 255) / 256;
