@@ -42,6 +42,8 @@
 namespace wp {
 namespace {
 
+constexpr int NTHREADS = 256;
+constexpr int K_WARP = 4, V_WARP = 5, QK_WARP = 6, PV_WARP = 7;
 constexpr int SUB = 64;  // keys per sub-tile
 constexpr int SMEM_PER_CTA = 115712;  // (228 KB - 2 x 1 KB reserved) / 2
 constexpr uint32_t TMEM_COLS = 256;  // two CTAs per SM share 512
@@ -82,6 +84,110 @@ __device__ __forceinline__ void keep_columns(uint32_t (&su)[64], uint64_t bits, 
   }
 }
 
+// Splits of a sequence: at most a.nsplit, each of at least MIN_KEYS keys.
+constexpr int MIN_KEYS = 256;
+__device__ __forceinline__ int sequence_splits(const TreeArgs &a, int tiles) {
+  constexpr int least = MIN_KEYS / SUB;
+  return max(1, min(a.nsplit, (tiles + least - 1) / least));
+}
+
+// Does a page of the keys [begin, end) lie outside the pool? Threads share the
+// entries, every one of them returns for its own.
+__device__ __forceinline__ bool bad_page(const CacheGeom &g, int b, int begin, int end, int thread, int threads) {
+  if (g.block_table == nullptr || begin >= end) return false;
+  bool bad = false;
+  for (int64_t j = begin / g.page_size + thread; j <= (end - 1) / g.page_size; j += threads)
+    bad = bad || cache_page(g, b, static_cast<int>(j * g.page_size)) < 0;
+  return bad;
+}
+
+struct Work {
+  int b, hk, k_begin, k_end, ntiles;  // sequence, KV head, the CTA's keys and key tiles
+  int first_row, nodes;               // first node of the CTA's rows; nodes of one Q box
+};
+
+// Producer of Q and K. Lane i looks up box i % boxes one tile ahead of its
+// loads (a block table's entry arrives meanwhile).
+template <int D, bool KGM>
+__device__ __forceinline__ void produce_k(const TreeMaps &tm, const TreeArgs &a, const Work &w, int len, uint8_t *q_smem,
+                                          uint32_t q_tile, uint64_t *q_full, uint8_t *ring_smem, uint64_t *k_full,
+                                          uint64_t *k_empty, volatile int *abort_flag) {
+  constexpr int G = D / 16;
+  constexpr uint32_t STAGE = SUB * D * 2;
+  const CacheGeom &cg = a.cache;
+  const int lane = threadIdx.x % 32, R = a.Hq / cg.Hkv;
+  const int box = a.box_rows, boxes = SUB / box, stages = a.k_stages;
+  const int my_cut = lane < G ? a.cut[lane] : 0;
+  const int key0 = w.k_begin + (lane & (boxes - 1)) * box;
+  const long long lim = a.wait_limit;
+  const bool leader = elect_one();
+  Ring ring;  // of the next load; a slot is free once its previous round was consumed
+  int issued = 0;
+  if (w.ntiles > 0 && leader) {
+    mbar_arrive_expect_tx(q_full, G * 32u * R * w.nodes);
+    for (int g = 0; g < G; ++g) tma_load_4d(q_smem + g * q_tile, &tm.q, q_full, 16 * g, w.hk * R, w.first_row, w.b);
+  }
+  __syncwarp();
+  Place here = place_of(cg, w.b, key0, w.k_end);
+  for (int u = 0; u < w.ntiles; ++u) {
+    const Place next = place_of(cg, w.b, key0 + (u + 1) * SUB, w.k_end);
+    uint64_t *full = &k_full[ring.slot];
+    uint8_t *dst = ring_smem + ring.slot * STAGE;
+    uint32_t need = live_groups<SUB>(my_cut, G, len, w.k_begin + u * SUB, lane);
+    if (!KGM) need = ((need & 0xfu) ? 1u : 0u) | ((need >> 4) ? 2u : 0u);  // 64-dim chunks
+    if (u >= stages && !warp_wait_idle(&k_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) break;
+    const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
+    if (leader) mbar_arrive_expect_tx(full, have * __popc(need) * box * (KGM ? 32u : 128u));
+    issue_k<D, KGM, SUB>(tm, here, have, need, box, w.hk, dst, full, leader);
+    ++issued;
+    ring.next(stages);
+    here = next;
+  }
+  // no bulk copy may still be in flight when this CTA's shared memory goes
+  if (w.ntiles > 0) warp_wait_idle(q_full, 0, drain_limit(a), nullptr);
+  for (int s = 0; s < stages && s < issued; ++s) {
+    const int last = s + ((issued - 1 - s) / stages) * stages;
+    warp_wait_idle(&k_full[s], (last / stages) & 1, drain_limit(a), nullptr);
+  }
+}
+
+// Producer of V: whole rows, one box after the other; within a box the 64-dim
+// chunks lie box * 128 bytes apart.
+template <int D>
+__device__ __forceinline__ void produce_v(const TreeMaps &tm, const TreeArgs &a, const Work &w, uint8_t *ring_smem,
+                                          uint64_t *v_full, uint64_t *v_empty, volatile int *abort_flag) {
+  constexpr uint32_t STAGE = SUB * D * 2;
+  const CacheGeom &cg = a.cache;
+  const int lane = threadIdx.x % 32;
+  const int box = a.box_rows, boxes = SUB / box, stages = a.v_stages;
+  const int key0 = w.k_begin + (lane & (boxes - 1)) * box;
+  const long long lim = a.wait_limit;
+  const bool leader = elect_one();
+  Ring ring;
+  int issued = 0;
+  Place here = place_of(cg, w.b, key0, w.k_end);
+  for (int u = 0; u < w.ntiles; ++u) {
+    const Place next = place_of(cg, w.b, key0 + (u + 1) * SUB, w.k_end);
+    uint64_t *full = &v_full[ring.slot];
+    if (u >= stages && !warp_wait_idle(&v_empty[ring.slot], ring.round ^ 1u, lim, abort_flag)) break;
+    const int have = __popc(__ballot_sync(FULL, lane < boxes && here.page >= 0));
+    if (leader) mbar_arrive_expect_tx(full, have * box * D * 2u);
+#pragma unroll 1
+    for (int i = 0; i < have; ++i) {
+      const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
+      if (leader) tma_load_5d(ring_smem + ring.slot * STAGE + i * box * D * 2, &tm.v, full, 0, row, 0, w.hk, page);
+      __syncwarp();
+    }
+    ++issued;
+    ring.next(stages);
+    here = next;
+  }
+  for (int s = 0; s < stages && s < issued; ++s) {
+    const int last = s + ((issued - 1 - s) / stages) * stages;
+    warp_wait_idle(&v_full[s], (last / stages) & 1, drain_limit(a), nullptr);
+  }
+}
+
 template <int D, bool KGM>
 __global__ void __launch_bounds__(NTHREADS, 2)
     tree_kernel(const __grid_constant__ TreeMaps tm, const __grid_constant__ TreeArgs a) {
@@ -113,7 +219,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   const int rows = min(a.tile_nodes, a.T - mt * a.tile_nodes) * R;  // up to 128
   const int warps = (rows + 31) / 32;                               // softmax warps with rows
   const Plan plan = sequence_plan<SUB>(a, b);
-  const int splits = sequence_splits<SUB>(a, plan.tiles);
+  const int splits = sequence_splits(a, plan.tiles);
   if (split >= splits) return;
   const int t_begin = static_cast<int>(static_cast<int64_t>(plan.tiles) * split / splits);
   const int nsub_all = static_cast<int>(static_cast<int64_t>(plan.tiles) * (split + 1) / splits) - t_begin;
@@ -175,9 +281,9 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   const int warp0 = warps == 1 ? half : warps == 2 ? 2 * half : 0;
 
   if (warp == K_WARP) {
-    produce_k<D, KGM, SUB>(tm, a, work, plan.len, smem + L.q_off, L.q_tile, q_full, smem, k_full, k_empty, abort_flag);
+    produce_k<D, KGM>(tm, a, work, plan.len, smem + L.q_off, L.q_tile, q_full, smem, k_full, k_empty, abort_flag);
   } else if (warp == V_WARP) {
-    produce_v<D, SUB>(tm, a, work, smem + L.v_off, v_full, v_empty, abort_flag);
+    produce_v<D>(tm, a, work, smem + L.v_off, v_full, v_empty, abort_flag);
   } else if (warp == QK_WARP) {
     // --------------------------------------------------------- issuer of S
     // S(u) into half u & 1, once P V(u - 2) has read the P that lies there.
@@ -190,7 +296,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     int bnd_cnt = 0;
     bool ok = nsub > 0 && warp_wait(q_full, 0, lim, abort_flag);
     const auto issue_groups = [&](uint32_t s_col, uint64_t kst_desc, uint32_t groups, uint32_t acc) {
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < G; ++g)
         if (groups & (1u << g)) {
           // K in rows: group g is 32 bytes into the 128-byte rows of chunk g / 4
@@ -476,7 +582,7 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const 
   if (row >= rows) return;
   const int64_t id = (static_cast<int64_t>(b) * a.cache.Hkv + hk) * rows + row;
   const Plan plan = sequence_plan<SUB>(a, b);
-  const int splits = sequence_splits<SUB>(a, plan.tiles);
+  const int splits = sequence_splits(a, plan.tiles);
   const float *lp = a.lse_part + id * a.nsplit;
   const float *op = a.o_part + id * a.nsplit * D + lane * E;
   float acc[E], sum = 0.f, M = -INFINITY;

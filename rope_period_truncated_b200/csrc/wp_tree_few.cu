@@ -1,10 +1,10 @@
-// Tree attention for few rows (nodes x query heads of a KV head <= 64), with
+// Tree attention for few rows (nodes x query heads of a KV head <= 32), with
 // the products turned round: S^T = K Q^T and O^T = V^T P^T.
 //
 // The mathematics is that of wp_tree.cu. With few rows an M = 128 tile of
 // query rows would be mostly padding, and its exponentials would sit in one
 // warp, 64 per thread and sub-tile. Here the 128 rows of a product are keys
-// (S^T) or head dims (O^T) and the query rows are its N (32 or 64): the tensor
+// (S^T) or head dims (O^T) and the query rows are its N = 32: the tensor
 // work shrinks with the rows, a softmax thread has one key and all rows, and
 // the four warps share a tile's exponentials evenly. HBM-bound.
 //
@@ -37,6 +37,7 @@ namespace wp {
 namespace {
 
 constexpr int TILE = 128;
+constexpr int NR = TREE_FEW_ROWS;  // query rows of a product
 constexpr int FEW_THREADS = 384;
 constexpr int FEW_K_WARP = 8, FEW_V_WARP = 9, FEW_QK_WARP = 10, FEW_PV_WARP = 11;
 constexpr int SMEM_CAP = 232448;  // dynamic shared memory of one CTA
@@ -48,15 +49,15 @@ constexpr uint32_t NUM_BARS = 2 + 4 * TREE_MAX_STAGES + 4 * 2 + TABLES + 7;
 
 // The nodes of one segment's sequence.
 struct NodeTable {
-  uint64_t seen_by[64];  // per node: the rows that see it
-  uint64_t upto[64];     // per depth: the rows no deeper
+  uint32_t seen_by[64];  // per node: the rows that see it
+  uint32_t upto[64];     // per depth: the rows no deeper
   int32_t depth[64];
   int deepest, bad, pad[2];
 };
 
 // Shared memory: K ring, V ring, two P tiles, Q (NR rows per group), then
 // the small tables and the barriers.
-template <int D, int NR>
+template <int D>
 struct FewLayout {
   static constexpr int G = D / 16;
   static constexpr uint32_t STAGE = TILE * D * 2;
@@ -142,33 +143,40 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-// TMEM columns [0, N) of this warp's lanes.
-template <int N>
-__device__ __forceinline__ void load_columns(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 64) {
-    tmem_ld64(taddr, r);
-  } else if constexpr (N == 32) {
-    tmem_ld32(taddr, r);
-    tmem_wait_ld(r);
-  } else {
-    tmem_ld16(taddr, r);
-  }
+// 32 TMEM columns of this warp's lanes.
+__device__ __forceinline__ void load_rows(uint32_t taddr, uint32_t (&r)[NR]) {
+  tmem_ld32(taddr, r);
+  tmem_wait_ld(r);
 }
-template <int N>
-__device__ __forceinline__ void store_columns(uint32_t taddr, const uint32_t (&r)[N]) {
-#pragma unroll
-  for (int c = 0; c < N; c += 32) tmem_st32(taddr + c, *reinterpret_cast<const uint32_t(*)[32]>(&r[c]));
+__device__ __forceinline__ void store_rows(uint32_t taddr, const uint32_t (&r)[NR]) {
+  tmem_st32(taddr, r);
   tmem_wait_st();
 }
 
 // Columns whose bit is clear become `fill`.
-template <int N>
-__device__ __forceinline__ void keep_rows(uint32_t (&r)[N], uint64_t bits, uint32_t fill) {
-  const uint32_t lo = static_cast<uint32_t>(bits), hi = static_cast<uint32_t>(bits >> 32);
+__device__ __forceinline__ void keep_rows(uint32_t (&r)[NR], uint32_t bits, uint32_t fill) {
 #pragma unroll
-  for (int c = 0; c < N; ++c)
-    if (!((c < 32 ? lo : hi) & (1u << (c & 31)))) r[c] = fill;
+  for (int c = 0; c < NR; ++c)
+    if (!(bits & (1u << c))) r[c] = fill;
 }
+
+// Lane i gets the sum over the warp of every lane's v[i]: at each step a lane
+// keeps half of its values and gives the other half away.
+__device__ __forceinline__ float warp_sums(float (&v)[32]) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float give = up ? v[i] : v[i + o], keep = up ? v[i + o] : v[i];
+      v[i] = keep + __shfl_xor_sync(FULL, give, o);
+    }
+  return v[0];
+}
+
+// Barrier `id` over `n` threads of the CTA (whole warps).
+__device__ __forceinline__ void named_sync(int id, int n) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // Floats as integers of the same order (and back).
 __device__ __forceinline__ int ordered(uint32_t x) {
@@ -176,10 +184,10 @@ __device__ __forceinline__ int ordered(uint32_t x) {
   return i ^ ((i >> 31) & 0x7fffffff);
 }
 
-template <int D, bool KGM, int NR>
+template <int D, bool KGM>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
     tree_few_kernel(const __grid_constant__ TreeMaps tm, const __grid_constant__ TreeArgs a) {
-  using L = FewLayout<D, NR>;
+  using L = FewLayout<D>;
   constexpr int G = D / 16;
   constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, NR, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, NR, true, true);
@@ -339,6 +347,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       const int end = min(seg.k_begin + seg.tiles * TILE, seg.plan.total);
       const int key0 = seg.k_begin + (lane & (boxes - 1)) * box;
       Place here = place_of(cg, seg.b, key0, end);
+#pragma unroll 1
       for (int u = 0; u < seg.tiles; ++u) {
         const Place next = place_of(cg, seg.b, key0 + (u + 1) * TILE, end);
         uint64_t *full = &k_full[ring.slot];
@@ -385,6 +394,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       ++q_issued;
       if (leader) bad_pages[seg.index % PAGE_FLAGS] = 0;
       __syncwarp();
+#pragma unroll 1
       for (int u = 0; u < seg.tiles; ++u) {
         const Place next = place_of(cg, seg.b, key0 + (u + 1) * TILE, end);
         uint64_t *full = &v_full[ring.slot];
@@ -399,6 +409,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           if (bad) bad_pages[seg.index % PAGE_FLAGS] = 1;
           mbar_arrive_expect_tx(full, have * box * D * 2u);
         }
+#pragma unroll 1
         for (int i = 0; i < have; ++i) {
           const int page = __shfl_sync(FULL, here.page, i), row = __shfl_sync(FULL, here.row, i);
           if (leader) tma_load_5d(smem + lay.v_off + ring.slot * L::STAGE + i * box * D * 2, &tm.v, full, 0, row, 0, seg.hk, page);
@@ -444,16 +455,17 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       __syncwarp();
       const int deepest = tab.deepest;
       {
-        const int r0 = lane, r1 = lane + 32;
-        const uint64_t m0 = r0 < rows ? sees[r0 / R] : 0ull, m1 = r1 < rows ? sees[r1 / R] : 0ull;
-        const int d0 = r0 < rows ? tab.depth[r0 / R] : 64, d1 = r1 < rows ? tab.depth[r1 / R] : 64;
+        const uint64_t mine = lane < rows ? sees[lane / R] : 0ull;
+        const int my_depth = lane < rows ? tab.depth[lane / R] : 64;
+#pragma unroll 1
         for (int u = 0; u < seg.plan.n; ++u) {
-          const uint64_t lo = __ballot_sync(FULL, (m0 >> u) & 1), hi = __ballot_sync(FULL, (m1 >> u) & 1);
-          if (lane == 0) tab.seen_by[u] = hi << 32 | lo;
+          const uint32_t set = __ballot_sync(FULL, (mine >> u) & 1);
+          if (lane == 0) tab.seen_by[u] = set;
         }
+#pragma unroll 1
         for (int u = 0; u <= deepest; ++u) {
-          const uint64_t lo = __ballot_sync(FULL, d0 <= u), hi = __ballot_sync(FULL, d1 <= u);
-          if (lane == 0) tab.upto[u] = hi << 32 | lo;
+          const uint32_t set = __ballot_sync(FULL, my_depth <= u);
+          if (lane == 0) tab.upto[u] = set;
         }
         if (lane == 0) tab.bad = bad;
         __syncwarp();
@@ -511,7 +523,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     // chunks box * 128 B apart. At d = 64 there is one chunk, and the upper 64
     // rows of O^T repeat the lower ones. B = P^T: rows contiguous.
     const uint64_t v_desc = smem_desc(smem_u32(smem + lay.v_off), D == 128 ? box * 128 : 0, 1024, SMEM_SWIZZLE_128B);
-    const uint64_t p_desc = smem_desc(smem_u32(smem + lay.p_off), 0, 8 * NR * 2, NR == 64 ? SMEM_SWIZZLE_128B : SMEM_SWIZZLE_64B);
+    const uint64_t p_desc = smem_desc(smem_u32(smem + lay.p_off), 0, 8 * NR * 2, SMEM_SWIZZLE_64B);
     Ring ring;
     int it = 0;
     bool ok = true;
@@ -524,7 +536,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < TILE / 16; ++kk)
             umma_ss(tmem + COL_O + NR * hh, vst_desc + v_step<D>(kk, box), pst_desc + kk * ((16 * NR * 2) >> 4), IDESC_PV,
                     (u > 1 || kk > 0) ? 1u : 0u);  // each stream's first tile of the segment starts O^T
@@ -582,17 +594,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
           while (ok && next_boundary_class(a.cut, cls >> 8, prev, &W, &groups)) {
             // rows within the window: len + depth - kpos <= W
             const int64_t most = W + kpos - plan.len;
-            const uint64_t keep = most < 0 ? 0ull : tab.upto[static_cast<int>(min(most, static_cast<int64_t>(deepest)))];
+            const uint32_t keep = most < 0 ? 0u : tab.upto[static_cast<int>(min(most, static_cast<int64_t>(deepest)))];
             ok = warp_wait(&bnd_ready[hh], bnd_cnt & 1, lim, abort_flag);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int p = 0; p < NR; p += 32) {
-              uint32_t su[32];
-              load_columns<32>(s_addr + p, su);
-              keep_rows<32>(su, keep >> p, 0u);
-              store_columns<32>(s_addr + p, su);
-            }
+            uint32_t su[NR];
+            load_rows(s_addr, su);
+            keep_rows(su, keep, 0u);
+            store_rows(s_addr, su);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bnd_done[hh]);
@@ -602,95 +611,83 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
         ok = ok && warp_wait(&s_ready[hh], (it >> 1) & 1, lim, abort_flag);
         tc_fence_after();
-        const uint64_t visible = !drafts || context ? ~0ull : there ? tab.seen_by[key - plan.len] : 0ull;
+        const uint32_t visible = !drafts || context ? ~0u : there ? tab.seen_by[key - plan.len] : 0u;
         uint8_t *p_row = smem + lay.p_off + hh * L::P_TILE + kt * (NR * 2);
-        const int turn = NR == 64 ? (kt & 7) : ((kt >> 1) & 3);  // the swizzle of the row's 16-byte pieces
-        bool gone = false;
+        const int turn = (kt >> 1) & 3;  // the swizzle of the row's 16-byte pieces
+        uint32_t su[NR];
+        if (cls == 0) {  // no product: zeros, by the same load
 #pragma unroll
-        for (int part = 0; part < NR / 32; ++part) {  // 32 rows at a time, for the registers' sake
-          const int c0 = 32 * part;
-          uint32_t su[32];
-          if (cls == 0) {  // no product: zeros, by the same load
+          for (int c = 0; c < NR; ++c) su[c] = 0u;
+          store_rows(s_addr, su);
+        }
+        load_rows(s_addr, su);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[hh]);
+        if (drafts) keep_rows(su, visible, 0xff800000u);
+        // Does any logit exceed its row's maximum by more than 2^8?
+        float over = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) su[c] = 0u;
-            store_columns<32>(s_addr + c0, su);
+        for (int c = 0; c < NR; c += 4) {
+          const float4 m4 = *reinterpret_cast<const float4 *>(negm + c);
+          float x0, x1, x2, x3;
+          unpack_f2(ffma2(pack_f2(__uint_as_float(su[c]), __uint_as_float(su[c + 1])), c2x2, pack_f2(m4.x, m4.y)), x0, x1);
+          unpack_f2(ffma2(pack_f2(__uint_as_float(su[c + 2]), __uint_as_float(su[c + 3])), c2x2, pack_f2(m4.z, m4.w)), x2, x3);
+          over = max3(over, max3(x0, x1, x2), x3);
+        }
+        if (named_any(bar, 128, over > RESCALE_THRESHOLD || !ok)) {
+          if (named_any(bar, 128, !ok)) {
+            ok = false;
+            break;
           }
-          load_columns<32>(s_addr + c0, su);
-          if (part == NR / 32 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[hh]);
+          int *warp_max = reinterpret_cast<int *>(part4) + w4 * NR;
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            const int mx = __reduce_max_sync(FULL, ordered(su[c]));
+            if (lane == c) warp_max[c] = mx;
           }
-          if (drafts) keep_rows<32>(su, visible >> c0, 0xff800000u);
-          // Does any logit exceed its row's maximum by more than 2^8?
-          float over = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 m4 = *reinterpret_cast<const float4 *>(negm + c0 + c);
-            float x0, x1, x2, x3;
-            unpack_f2(ffma2(pack_f2(__uint_as_float(su[c]), __uint_as_float(su[c + 1])), c2x2, pack_f2(m4.x, m4.y)), x0, x1);
-            unpack_f2(ffma2(pack_f2(__uint_as_float(su[c + 2]), __uint_as_float(su[c + 3])), c2x2, pack_f2(m4.z, m4.w)), x2, x3);
-            over = max3(over, max3(x0, x1, x2), x3);
+          named_sync(bar, 128);
+          if (st < NR) {
+            const int *p = reinterpret_cast<const int *>(part4) + st;
+            const int mx = max(max(p[0], p[NR]), max(p[2 * NR], p[3 * NR]));
+            const float m_old = -negm[st];
+            const float m_new = fmaxf(m_old, __int_as_float(ordered(static_cast<uint32_t>(mx))) * c2);
+            alpha[st] = fast_exp2(m_old - m_new);
+            negm[st] = -m_new;
           }
-          if (named_any(bar, 128, over > RESCALE_THRESHOLD || !ok)) {
-            if (named_any(bar, 128, !ok)) {
-              gone = true;
-              break;
-            }
-            int *warp_max = reinterpret_cast<int *>(part4) + w4 * NR + c0;
+          named_sync(bar, 128);
+          if (!fresh) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int mx = __reduce_max_sync(FULL, ordered(su[c]));
-              if (lane == c) warp_max[c] = mx;
+            for (int c = 0; c < NR; c += 2) {
+              float l0, l1;
+              unpack_f2(l2[c / 2], l0, l1);
+              l2[c / 2] = pack_f2(l0 * alpha[c], l1 * alpha[c + 1]);
             }
-            named_sync(bar, 128);
-            if (st < 32) {
-              const int r = c0 + st;
-              const int *p = reinterpret_cast<const int *>(part4) + r;
-              const int mx = max(max(p[0], p[NR]), max(p[2 * NR], p[3 * NR]));
-              const float m_old = -negm[r];
-              const float m_new = fmaxf(m_old, __int_as_float(ordered(static_cast<uint32_t>(mx))) * c2);
-              alpha[r] = fast_exp2(m_old - m_new);
-              negm[r] = -m_new;
-            }
-            named_sync(bar, 128);
-            if (!fresh) {
+            ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag);  // the stream's last P V
+            tc_fence_after();
+            uint32_t ov[NR];
+            load_rows(o_addr, ov);
 #pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                float l0, l1;
-                unpack_f2(l2[(c0 + c) / 2], l0, l1);
-                l2[(c0 + c) / 2] = pack_f2(l0 * alpha[c0 + c], l1 * alpha[c0 + c + 1]);
-              }
-              ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag);  // the stream's last P V
-              tc_fence_after();
-              uint32_t ov[32];
-              load_columns<32>(o_addr + c0, ov);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha[c0 + c]);
-              store_columns<32>(o_addr + c0, ov);
-            }
-          }
-          // P^T of two tiles ago must have been read before its place is written again
-          if (part == 0 && it >= 2) ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag) && ok;
-#pragma unroll
-          for (int c = c0; c < c0 + 32; c += 8) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = c - c0 + 2 * e;
-              const uint64_t m2 = *reinterpret_cast<const uint64_t *>(negm + c + 2 * e);
-              float x0, x1;
-              unpack_f2(ffma2(pack_f2(__uint_as_float(su[i]), __uint_as_float(su[i + 1])), c2x2, m2), x0, x1);
-              const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-              l2[c / 2 + e] = fadd2(l2[c / 2 + e], pack_f2(p0, p1));
-              w[e] = pack_bf16x2(p0, p1);
-            }
-            *reinterpret_cast<uint4 *>(p_row + (((c >> 3) ^ turn) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int c = 0; c < NR; ++c) ov[c] = __float_as_uint(__uint_as_float(ov[c]) * alpha[c]);
+            store_rows(o_addr, ov);
           }
         }
-        if (gone) {
-          ok = false;
-          break;
+        // P^T of two tiles ago must have been read before its place is written again
+        if (it >= 2) ok = warp_wait(&o_ready[hh], ((it >> 1) - 1) & 1, lim, abort_flag) && ok;
+#pragma unroll
+        for (int c = 0; c < NR; c += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = c + 2 * e;
+            const uint64_t m2 = *reinterpret_cast<const uint64_t *>(negm + i);
+            float x0, x1;
+            unpack_f2(ffma2(pack_f2(__uint_as_float(su[i]), __uint_as_float(su[i + 1])), c2x2, m2), x0, x1);
+            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            l2[i / 2] = fadd2(l2[i / 2], pack_f2(p0, p1));
+            w[e] = pack_bf16x2(p0, p1);
+          }
+          *reinterpret_cast<uint4 *>(p_row + (((c >> 3) ^ turn) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         fresh = false;
         if (u == seg.tiles - 1) {
@@ -717,13 +714,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       // the factors that bring the two accumulators to one maximum, and half
       // of the rows' results each.
       ok = ok && warp_wait(o_final, seg.index & 1, lim, abort_flag);
+      float l[NR];
 #pragma unroll
-      for (int c0 = 0; c0 < NR; c0 += 32) {
-        float l[32];
-#pragma unroll
-        for (int c = 0; c < 32; c += 2) unpack_f2(l2[(c0 + c) / 2], l[c], l[c + 1]);
-        part4[w4 * NR + c0 + lane] = warp_sums(l);
-      }
+      for (int c = 0; c < NR; c += 2) unpack_f2(l2[c / 2], l[c], l[c + 1]);
+      part4[w4 * NR + lane] = warp_sums(l);
       ok = !named_any(1, 256, !ok);  // all eight warps or none
       if (!ok) *abort_flag = 1;
       tc_fence_after();
@@ -751,8 +745,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
       constexpr int HALF = NR / 2;
       uint32_t ov[2][HALF];
       const uint32_t half_addr = lane_addr + COL_O + hh * HALF;
-      load_columns<HALF>(half_addr, ov[0]);
-      load_columns<HALF>(half_addr + NR, ov[1]);
+      tmem_ld16(half_addr, ov[0]);
+      tmem_ld16(half_addr + NR, ov[1]);
 #pragma unroll
       for (int c = 0; c < HALF; ++c) {
         const float f0 = all_alpha[hh * HALF + c], f1 = all_alpha[NR + hh * HALF + c];
@@ -861,24 +855,24 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_few_merge_kernel(const 
     *lse = spoilt ? __int_as_float(0x7fc00000) : live ? (M + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
-template <int D, bool KGM, int NR>
+template <int D, bool KGM>
 cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
-  using L = FewLayout<D, NR>;
+  using L = FewLayout<D>;
   // as many stages as fit, one more of K than of V where the number is odd
   const int fit = (SMEM_CAP - static_cast<int>(L::FIXED)) / static_cast<int>(L::STAGE);
   const int stages = fit < 2 * TREE_MAX_STAGES ? fit : 2 * TREE_MAX_STAGES;
   a.v_stages = stages / 2;
   a.k_stages = stages - a.v_stages;
   const int smem = static_cast<int>(L::FIXED + stages * L::STAGE);
-  const cudaError_t e = allow_shared_memory<tree_few_kernel<D, KGM, NR>>(SMEM_CAP);
+  const cudaError_t e = allow_shared_memory<tree_few_kernel<D, KGM>>(SMEM_CAP);
   if (e != cudaSuccess) return e;
-  tree_few_kernel<D, KGM, NR><<<a.nsplit, FEW_THREADS, smem, stream>>>(tm, a);
+  tree_few_kernel<D, KGM><<<a.nsplit, FEW_THREADS, smem, stream>>>(tm, a);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_both(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
-  const cudaError_t e = a.cache.k_group_major ? launch<D, true, TREE_FEW_ROWS>(tm, a, stream) : launch<D, false, TREE_FEW_ROWS>(tm, a, stream);
+  const cudaError_t e = a.cache.k_group_major ? launch<D, true>(tm, a, stream) : launch<D, false>(tm, a, stream);
   if (e != cudaSuccess || a.prefix == nullptr) return e;
   // started while the first kernel runs; it waits for its results on the device
   const int rows = a.T * (a.Hq / a.cache.Hkv);
