@@ -101,8 +101,9 @@ struct PagesArgs {
   int32_t *writers, *first, *order;          // scratch [n_pages] each
   int32_t *off, *copying;            // scratch [B] each
   int B, max_pages, n_pages, page_size;
+  int in_shared;                     // the scratch is the block's shared memory; set at the launch
 };
-cudaError_t launch_pages_update(const PagesArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_update(PagesArgs a, cudaStream_t stream);
 
 struct PagesCopyArgs {
   CacheGeom cache;

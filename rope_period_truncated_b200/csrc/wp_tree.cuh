@@ -130,7 +130,6 @@ template <int D, bool KGM, int TILE>
 __device__ __forceinline__ void issue_k(const TreeMaps &tm, const Place &here, int have, uint32_t need, int box, int hk,
                                         uint8_t *dst, uint64_t *full, bool leader) {
   constexpr uint32_t GROUP = TILE * 32, CHUNK = TILE * 128;
-  constexpr int PIECES = KGM ? D / 16 : D / 64;
   if (box == TILE) {
     const int page = __shfl_sync(FULL, here.page, 0), row = __shfl_sync(FULL, here.row, 0);
     if (leader && have) {
