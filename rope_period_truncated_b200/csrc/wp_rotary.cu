@@ -17,7 +17,9 @@
 // thread keeps one token and one unit and walks over the heads, two in flight,
 // its 8 (cos, sin) in registers; read from shared memory for every unit they
 // were what bounded the kernel (131 us against 112).
-// Q and K of 32768 tokens, 32 + 8 heads of 128: 105 us, 6.4 TB/s.
+// Q and K of 32768 tokens, 32 + 8 heads of 128: 105 us, 6.4 TB/s. Appending 20005
+// tokens of the same heads, half of each head rotated, to pages of 16 keys: 70
+// us, 5.8 TB/s; 128 tokens: 4 us.
 #include <cuda_bf16.h>
 #include <cstdint>
 

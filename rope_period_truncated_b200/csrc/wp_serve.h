@@ -99,9 +99,9 @@ struct PagesArgs {
   int32_t *refs_out, *table_out, *lens_out, *copies, *info;
   unsigned long long *counts;                // scratch [n_pages]
   int32_t *writers, *first, *order;          // scratch [n_pages] each
-  int32_t *off, *copying;            // scratch [B] each
+  int32_t *off, *copying;                    // scratch [B] each
   int B, max_pages, n_pages, page_size;
-  int in_shared;                     // the scratch is the block's shared memory; set at the launch
+  int in_shared;                             // the scratch is the block's shared memory; set at the launch
 };
 cudaError_t launch_pages_update(PagesArgs a, cudaStream_t stream);
 
@@ -134,14 +134,18 @@ struct TreeArgs {
 };
 
 // How the work is cut. Up to 32 rows per KV head (R query heads of T nodes) go
-// to the kernel whose products have keys and dims as their 128 rows: tiles of
-// 128 keys, one CTA per SM, the tiles of all sequences and KV heads dealt out
-// evenly; or, where no sequence can exceed 512 keys and the (sequence, KV head)
-// units are no more than the SMs, a CTA per unit, which needs no merge (its
-// launch and run cost 5 us, a tile about 1). More rows go to the one that has
-// query rows there: tiles of whole nodes, 64 keys, two CTAs per SM, each
-// (sequence, KV head) split on its own: so that the CTAs fill the SMs once (256
-// of 296 places: 4 x 2.5K to 4K keys 30.7 us with 9 splits, 28.4 with 8), or,
+// to the kernel whose products have keys and dims as their 128 rows (16
+// sequences of 16K to 32K keys, 32 rows: 211 us, 239 with the other; with 64
+// rows, which it then took, 318 against 264): tiles of 128 keys, one CTA per SM,
+// the tiles of all sequences and KV heads dealt out evenly; or, where no sequence
+// can exceed 512 keys and the (sequence, KV head) units are no more than the
+// SMs, a CTA per unit, which needs no merge (its launch and run cost 5 us, a
+// tile about 1). More rows go to the one that has query rows there: tiles of
+// whole nodes, 64 keys, two CTAs per SM, each
+// (sequence, KV head) split on its own: so that the CTAs fill the SMs once (all
+// 296 places where a CTA then has at least 1024 keys: 252 rows over 128K keys
+// 146 us, 159 with 256 CTAs; else 256, with less to merge: 4 x 2.5K to 4K keys
+// 30.7 us with 9 splits, 28.4 with 8), or,
 // for several sequences, whose lengths may differ, up to twice as long as a CTA
 // keeps 1024 keys (16 x 16K to 32K keys, 64 rows: 248 us, 261 with twice as many).
 constexpr int TREE_FEW_ROWS = 32;
@@ -160,7 +164,8 @@ inline int tree_splits(int B, int T, int Hkv, int R, int64_t capacity) {
     return static_cast<int>(tiles < TREE_SMS ? tiles : TREE_SMS);
   }
   const int tile = tree_tile_nodes(T, R), row_tiles = (T + tile - 1) / tile;
-  const int64_t once = 256 / (units * row_tiles);
+  int64_t once = 2 * TREE_SMS / (units * row_tiles);
+  if (once * 1024 > capacity) once = 256 / (units * row_tiles);
   int64_t n = B == 1 ? 0 : 4 * TREE_SMS / (units * row_tiles);
   if (n > capacity / 1024) n = capacity / 1024;
   if (n < once) n = once;
