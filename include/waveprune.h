@@ -557,7 +557,8 @@ size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, 
  *                [B, H_q, T] (natural log, scale included), or NULL.
  *   workspace    device scratch of at least wp_decode_tree_workspace_bytes(...)
  *                bytes, 256-byte aligned (may be NULL where that is 0);
- *                contents on entry do not matter.
+ *                contents on entry do not matter. Calls that may run at the
+ *                same time need workspaces of their own.
  * o, lse and the workspace overlap nothing else.
  * A sequence whose length, node count, parents or pages are out of range gets
  * NaN rows (nothing is read through them). A wait that gives up records
@@ -623,7 +624,8 @@ size_t wp_pages_update_workspace_bytes(int B, int n_pages);
  * If the free pages do not suffice (WP_PAGES_SHORT) or an entry is out of
  * range (WP_PAGES_BAD_ARGUMENT), nothing changes: the outputs are the inputs
  * and copies is empty. No output overlaps an input, another output or the
- * workspace (8-byte aligned; contents on entry do not matter).
+ * workspace (8-byte aligned; contents on entry do not matter; calls that may run
+ * at the same time need workspaces of their own).
  * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED (capacity or n_pages above 2^30, B
  * above 65535), WP_ERR_CUDA.
  */
