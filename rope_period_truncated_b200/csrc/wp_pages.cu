@@ -79,6 +79,7 @@ __device__ __forceinline__ int holders(int refs, unsigned long long counts) {
 __device__ __forceinline__ int copies_of(int r, int w) { return r > 1 ? (w == r ? w - 1 : w) : 0; }
 
 __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_constant__ PagesArgs a) {
+  cudaGridDependencySynchronize();
   // One block: its scratch and the holders' counts are in shared memory, for the
   // atomics and for the reads that wait for them. 16 rows, a pool of 640 pages:
   // 11.5 -> 7.5 us.
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
 constexpr int COPY_THREADS = 256;
 
 __global__ void __launch_bounds__(COPY_THREADS) pages_copy_kernel(const __grid_constant__ PagesCopyArgs a) {
+  cudaGridDependencySynchronize();
   const CacheGeom &g = a.cache;
   const int i = blockIdx.x, h = blockIdx.y;
   const int32_t *c = a.copies + 3 * static_cast<int64_t>(i);
@@ -329,6 +331,7 @@ constexpr int COMPACT_THREADS = 256;
 constexpr int BATCH = 8;
 
 __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const __grid_constant__ CompactArgs a) {
+  cudaGridDependencySynchronize();
   // element offsets of head 0, dim 0: of V; of K the same in rows, else apart
   __shared__ int64_t s_from[COMPACT_MAX_PATH], s_to[COMPACT_MAX_PATH];
   __shared__ int s_row_from[COMPACT_MAX_PATH], s_row_to[COMPACT_MAX_PATH];
@@ -399,33 +402,22 @@ cudaError_t launch_pages_update(PagesArgs a, cudaStream_t stream) {
   const int64_t work = a.n_pages + static_cast<int64_t>(a.B) * a.max_pages;
   int blocks = 1;
   while (work >= ONE_BLOCK && blocks < MAX_CLUSTER && blocks <= work / PER_BLOCK) blocks *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(PG_THREADS);
+  size_t smem = 0;
   a.in_shared = blocks == 1;
   if (a.in_shared) {
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.n_pages) * 24 + static_cast<size_t>(a.B) * 8;
+    smem = static_cast<size_t>(a.n_pages) * 24 + static_cast<size_t>(a.B) * 8;
     const cudaError_t e = allow_shared_memory<pages_update_kernel>(ONE_BLOCK * 24);  // n_pages + B < ONE_BLOCK
     if (e != cudaSuccess) return e;
   }
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = blocks;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = blocks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, pages_update_kernel, a);
+  return launch_after(pages_update_kernel, dim3(blocks), PG_THREADS, smem, stream, blocks, a);
 }
 
 cudaError_t launch_pages_copy(const PagesCopyArgs &a, cudaStream_t stream) {
-  pages_copy_kernel<<<dim3(a.n, a.cache.Hkv), COPY_THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(pages_copy_kernel, dim3(a.n, a.cache.Hkv), COPY_THREADS, 0, stream, 1, a);
 }
 
 cudaError_t launch_compact(const CompactArgs &a, cudaStream_t stream) {
-  compact_kernel<<<a.cache.B, COMPACT_THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(compact_kernel, dim3(a.cache.B), COMPACT_THREADS, 0, stream, 1, a);
 }
 
 }  // namespace wp

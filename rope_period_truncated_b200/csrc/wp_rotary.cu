@@ -96,6 +96,7 @@ __device__ __forceinline__ void rotate_unit(Unit &x, const float2 (&w)[8]) {
 // heads, then tokens.
 template <int D, bool PAIRS_IN, bool PAIRS_OUT, bool APPEND>
 __global__ void __launch_bounds__(THREADS, 6) rotary_kernel(const __grid_constant__ RotaryArgs a, int log_tokens) {
+  cudaGridDependencySynchronize();
   constexpr int ULOG = D == 128 ? 3 : 2, U = 1 << ULOG;  // units per head
   extern __shared__ float2 cs[];                        // [tokens][rot / 2]
   __shared__ TokenPlace places[MAX_TOKENS];
@@ -226,11 +227,8 @@ cudaError_t launch(const RotaryArgs &a, bool append, cudaStream_t stream) {
   const int64_t blocks = (a.tokens + (1 << log_tokens) - 1) >> log_tokens;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const size_t smem = (static_cast<size_t>(a.rot / 2) << log_tokens) * sizeof(float2);
-  if (append)
-    rotary_kernel<D, PAIRS_IN, PAIRS_OUT, true><<<static_cast<unsigned>(blocks), THREADS, smem, stream>>>(a, log_tokens);
-  else
-    rotary_kernel<D, PAIRS_IN, PAIRS_OUT, false><<<static_cast<unsigned>(blocks), THREADS, smem, stream>>>(a, log_tokens);
-  return cudaGetLastError();
+  const auto kernel = append ? rotary_kernel<D, PAIRS_IN, PAIRS_OUT, true> : rotary_kernel<D, PAIRS_IN, PAIRS_OUT, false>;
+  return launch_after(kernel, dim3(static_cast<unsigned>(blocks)), THREADS, smem, stream, 1, a, log_tokens);
 }
 
 template <int D>

@@ -201,6 +201,7 @@ __device__ __forceinline__ void produce_v(const TreeMaps &tm, const TreeArgs &a,
 template <int D, bool KGM>
 __global__ void __launch_bounds__(NTHREADS, 2)
     tree_kernel(const __grid_constant__ TreeMaps tm, const __grid_constant__ TreeArgs a) {
+  cudaGridDependencySynchronize();
   constexpr int G = D / 16;
   constexpr uint32_t STAGE = Layout<D>::STAGE;
   constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, SUB, false, false);
@@ -647,23 +648,13 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
   const cudaError_t e = allow_shared_memory<tree_kernel<D, KGM>>(SMEM_PER_CTA);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.row_tiles * a.nsplit, a.cache.Hkv, a.B);
-  tree_kernel<D, KGM><<<grid, NTHREADS, smem, stream>>>(tm, a);
-  return cudaGetLastError();
+  return launch_after(tree_kernel<D, KGM>, grid, NTHREADS, smem, stream, 1, tm, a);
 }
 
 template <int D>
 cudaError_t combine(const TreeArgs &a, cudaStream_t stream) {
-  // started while the first kernel runs; it waits for its results on the device
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.T * (a.Hq / a.cache.Hkv) + COMBINE_WARPS - 1) / COMBINE_WARPS, a.cache.Hkv, a.B);
-  cfg.blockDim = dim3(COMBINE_WARPS * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, a);
+  const dim3 grid((a.T * (a.Hq / a.cache.Hkv) + COMBINE_WARPS - 1) / COMBINE_WARPS, a.cache.Hkv, a.B);
+  return launch_after(tree_combine_kernel<D>, grid, COMBINE_WARPS * 32, 0, stream, 1, a);
 }
 
 }  // namespace

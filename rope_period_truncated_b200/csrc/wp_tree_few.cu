@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     mbar_init(o_final, 1);
     fence_barrier_init();
   }
+  cudaGridDependencySynchronize();  // nothing of global memory before it, nor of TMEM, which the kernel before may hold
   if (warp == FEW_QK_WARP) {
     tmem_alloc(tmem_slot, TMEM_COLS);
     tmem_relinquish();
@@ -871,26 +872,16 @@ cudaError_t launch(const TreeMaps &tm, TreeArgs a, cudaStream_t stream) {
   const int smem = static_cast<int>(L::FIXED + stages * L::STAGE);
   const cudaError_t e = allow_shared_memory<tree_few_kernel<D, KGM>>(SMEM_CAP);
   if (e != cudaSuccess) return e;
-  tree_few_kernel<D, KGM><<<a.nsplit, FEW_THREADS, smem, stream>>>(tm, a);
-  return cudaGetLastError();
+  return launch_after(tree_few_kernel<D, KGM>, dim3(a.nsplit), FEW_THREADS, smem, stream, 1, tm, a);
 }
 
 template <int D>
 cudaError_t launch_both(const TreeMaps &tm, const TreeArgs &a, cudaStream_t stream) {
   const cudaError_t e = a.cache.k_group_major ? launch<D, true>(tm, a, stream) : launch<D, false>(tm, a, stream);
   if (e != cudaSuccess || a.prefix == nullptr) return e;
-  // started while the first kernel runs; it waits for its results on the device
   const int rows = a.T * (a.Hq / a.cache.Hkv);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((rows + MERGE_WARPS - 1) / MERGE_WARPS, a.cache.Hkv, a.B);
-  cfg.blockDim = dim3(MERGE_WARPS * 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_few_merge_kernel<D>, a, a.nsplit);
+  const dim3 grid((rows + MERGE_WARPS - 1) / MERGE_WARPS, a.cache.Hkv, a.B);
+  return launch_after(tree_few_merge_kernel<D>, grid, MERGE_WARPS * 32, 0, stream, 1, a, a.nsplit);
 }
 
 }  // namespace
