@@ -3,8 +3,8 @@
 // C ABI, whose function addresses the package hands over. These calls last a
 // few microseconds on the device at their smallest, so their marshalling is
 // compiled. Measured, us a call among others, here / marshalled in Python: a
-// rotation of 256 tokens 6.0 / 15, an append of 128 tokens 6.0 / 18, a tree of 4
-// nodes 10 / 17, an append with a compaction 10 / 30, a page step 17 / 28.
+// rotation of 256 tokens 6.0 / 15, an append of 128 tokens 6.0 / 18, an append
+// with a compaction 10 / 30, a page step of two calls 11 / 25.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

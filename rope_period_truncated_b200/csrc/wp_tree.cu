@@ -33,11 +33,11 @@
 // that P = 0 meets no NaN that an unused slot may hold.
 //
 // Splits write O (fp32) and LSE to the workspace; a second kernel merges them
-// (3 to 6 us; merging in a cluster through its shared memory took 7).
+// (4 to 7 us; merging in a cluster through its shared memory took 7 and more).
 //
 // What bounds it. Few splits of short caches: latency, about 3 us until the
 // first keys are there and 2 from the last product to the written rows (4
-// sequences of 2.5K to 4K keys, 64 rows: 27 us, of which the merge 3.4). 16
+// sequences of 2.5K to 4K keys, 64 rows: 25 us, of which the merge 4). 16
 // sequences of 16K to 32K keys, 64 rows: 241 us, 5.1 TB/s. 252 rows over 128K
 // keys, most groups live: 146 us, 600 TFLOP/s, a sub-tile in about 1760 cycles
 // per CTA: its products take 640 of the tensor core's (those of S at two thirds
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
   }
 }
 
-// One warp per row: O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M).
+// Merges the splits, one warp per row.
 constexpr int COMBINE_WARPS = 4;
 
 template <int D>
@@ -594,35 +594,12 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) tree_combine_kernel(const 
   const int64_t id = (static_cast<int64_t>(b) * a.cache.Hkv + hk) * rows + row;
   const Plan plan = sequence_plan<SUB>(a, b);
   const int splits = sequence_splits(a, plan.tiles);
-  const float *lp = a.lse_part + id * a.nsplit;
-  const float *op = a.o_part + id * a.nsplit * D + lane * E;
-  float acc[E], sum = 0.f, M = -INFINITY;
+  float acc[E], sum = 1.f, M = 0.f;
   bool spoilt = !plan.ok;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
   const bool there = plan.ok && row / R < plan.n;
   if (there) {
-    for (int s = lane; s < splits; s += 32) M = fmaxf(M, lp[s]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    merge_row<D>(a, splits, [&](int i) { return id * a.nsplit + i; }, acc, sum, M);
     spoilt = M == INFINITY;
-    for (int s = 0; s < splits; s += 4) {
-      float w[4], v[4][E];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int at = min(s + k, splits - 1);
-        const float l = lp[at];
-        w[k] = s + k >= splits || l == -INFINITY ? 0.f : fast_exp2(l - M);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = op[static_cast<int64_t>(at) * D + e];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        sum += w[k];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += w[k] * v[k][e];
-      }
-    }
   }
   __nv_bfloat16 *o = a.o + out_row(a, b, hk, R, row) * D + lane * E;
 #pragma unroll

@@ -217,5 +217,46 @@ __device__ __forceinline__ bool node_masks(const TreeArgs &a, const Plan &plan, 
   return bad;
 }
 
+// A warp merges `count` partial results of one row, partial i in slot(i): O =
+// sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M), E dims per lane. Eight at a time,
+// their LSE and rows loaded together, each time brought to the maximum so far: a
+// load takes as long as the arithmetic of all of them. M = infinity: spoilt.
+template <int D, class Slot>
+__device__ __forceinline__ void merge_row(const TreeArgs &a, int count, Slot slot, float (&acc)[D / 32], float &sum, float &M) {
+  constexpr int E = D / 32, BATCH = 8;
+  const int lane = threadIdx.x % 32;
+  M = -INFINITY;
+  sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < count; i += BATCH) {
+    float l[BATCH], v[BATCH][E];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const bool in = i + k < count;
+      const int64_t s = in ? slot(i + k) : 0;
+      l[k] = in ? a.lse_part[s] : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = in ? a.o_part[s * D + lane * E + e] : 0.f;
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) m = fmaxf(m, l[k]);
+    const float scale = M == -INFINITY ? 0.f : fast_exp2(M - m);
+    sum *= scale;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= scale;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float w = l[k] == -INFINITY ? 0.f : fast_exp2(l[k] - m);
+      sum += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] += w * v[k][e];
+    }
+    M = m;
+  }
+}
+
 }  // namespace
 }  // namespace wp

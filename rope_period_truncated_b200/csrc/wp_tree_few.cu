@@ -9,9 +9,10 @@
 // the four warps share a tile's exponentials evenly.
 //
 // What bounds it: HBM over long caches (16 sequences of 16K to 32K keys, 32 rows,
-// pages of 64 keys: 211 us, 5.9 TB/s; K in rows 255), the issue of the copies
-// where pages are small (32 keys 224 us, 16 keys 397), latency over short ones (4
-// sequences of 2.5K to 4K keys: 29 us; one of 200 keys, a CTA per KV head: 9).
+// pages of 64 keys: 211 us, 5.9 TB/s; K in rows, whose 64-dim chunks are read
+// whole, 256), the issue of the copies
+// where pages are small (32 keys 221 us, 16 keys 341), latency over short ones (4
+// sequences of 2.5K to 4K keys: 27 us; one of 200 keys, a CTA per KV head: 9).
 //
 // One CTA per SM. All (sequence, KV head) units lie end to end as a line of
 // 128-key tiles, cut evenly among the CTAs, whatever the lengths: a CTA walks
@@ -793,9 +794,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 }
 
 // Merges the partial results of the units that more than one CTA worked on, one
-// warp per row: O = sum_s 2^(lse_s - M) O_s / sum_s 2^(lse_s - M). It also
-// writes the rows that no CTA had: of sequences without nodes, or with bad
-// lengths.
+// warp per row. It also writes the rows that no CTA had: of sequences without
+// nodes, or with bad lengths.
 constexpr int MERGE_WARPS = 4;
 
 template <int D>
@@ -809,8 +809,6 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_few_merge_kernel(const 
   const int64_t before = a.prefix[b], own = a.prefix[b + 1] - before, tiles = a.prefix[a.B] * a.cache.Hkv;
   float acc[E], sum = 1.f, M = 0.f;
   bool spoilt = false, live = false;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
   if (own == 0) {
     spoilt = !sequence_plan<TILE>(a, b).ok;
   } else {
@@ -819,35 +817,15 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) tree_few_merge_kernel(const 
     if (c0 == c1) return;  // that CTA wrote the rows
     // CTA c's slot: its first segment, or for a unit that begins within c0 its last
     const int late = cut(tiles, c0, G) < x0 ? 1 : 0;
-    const auto slot_of = [&](int c) { return static_cast<int64_t>(2 * c + (c == c0 ? late : 0)) * rows + row; };
-    // with fewer tiles than CTAs some of them have none
-    const auto has = [&](int c) { return c <= c1 && (tiles >= G || cut(tiles, c, G) < cut(tiles, c + 1, G)); };
     live = row / R < (a.n_nodes != nullptr ? a.n_nodes[b] : a.T);
-    M = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32)
-      if (has(c)) M = fmaxf(M, a.lse_part[slot_of(c)]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+    // with fewer tiles than CTAs some of them have none: then each of the unit's tiles is a part
+    const bool each = tiles < G;
+    const auto slot_of = [&](int i) {
+      const int c = each ? cta_of(tiles, x0 + i, G) : c0 + i;
+      return static_cast<int64_t>(2 * c + (c == c0 ? late : 0)) * rows + row;
+    };
+    merge_row<D>(a, each ? static_cast<int>(own) : c1 - c0 + 1, slot_of, acc, sum, M);
     spoilt = M == INFINITY;
-    sum = 0.f;
-    for (int c = c0; c <= c1; c += 4) {
-      float w[4], v[4][E];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool in = has(c + k);
-        const int64_t s = slot_of(in ? c + k : c0);  // c0 has a slot
-        const float l = a.lse_part[s];
-        w[k] = !in || l == -INFINITY ? 0.f : fast_exp2(l - M);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = a.o_part[s * D + lane * E + e];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        sum += w[k];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += w[k] * v[k][e];
-      }
-    }
   }
   __nv_bfloat16 *o = a.o + out_row(a, b, hk, R, row) * D + lane * E;
 #pragma unroll
