@@ -10,9 +10,9 @@
 //
 // What bounds it: HBM over long caches (16 sequences of 16K to 32K keys, 32 rows,
 // pages of 64 keys: 211 us, 5.9 TB/s; K in rows, whose 64-dim chunks are read
-// whole, 256), the issue of the copies
-// where pages are small (32 keys 221 us, 16 keys 341), latency over short ones (4
-// sequences of 2.5K to 4K keys: 27 us; one of 200 keys, a CTA per KV head: 9).
+// whole, 256), the issue of the copies where pages are small (32 keys 221 us, 16
+// keys 341), latency over short ones (4 sequences of 2.5K to 4K keys: 27 us; one
+// of 200 keys, a CTA per KV head: 9).
 //
 // One CTA per SM. All (sequence, KV head) units lie end to end as a line of
 // 128-key tiles, cut evenly among the CTAs, whatever the lengths: a CTA walks
