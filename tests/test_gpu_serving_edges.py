@@ -143,3 +143,48 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         wp.wp_pages_update(lens, par, lens, lens, lens, _i32([1]), 16)
     assert wp.wp_device_status() == 0
+
+
+@pytest.mark.parametrize("T,Hq", [(3, 4), (20, 4)])
+def test_steps_without_waiting_between_them(T, Hq):
+    """Each kernel is set up while the one before it ends: thirty steps enqueued at once give what they give one by one."""
+    B, Hkv, d, P, MP, pool = 5, 2, 64, 16, 40, 260
+
+    def steps(wait):
+        g = torch.Generator(device="cuda").manual_seed(4)
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        k, v = (torch.zeros(pool, Hkv, P, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        refs, table = torch.zeros(pool, dtype=torch.int32, device="cuda"), torch.full((B, MP), -1, dtype=torch.int32, device="cuda")
+        held, lens = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+        rows, node = torch.arange(B, dtype=torch.int32, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda")
+        seq, parents = rows.repeat_interleave(T), (node - 1).repeat(B, 1)
+        path = torch.arange(0, T, 2, dtype=torch.int32, device="cuda").repeat(B, 1)
+        outs = []
+        for i in range(30):
+            q, kn, vn = (torch.randn(B * T, h, d, generator=g, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+            pause()
+            parent = rows if i % 7 else rows.flip(0)
+            keep = lens[parent.long()]
+            pause()
+            refs, table, held, copies, info = wp.wp_pages_update(refs, table, held, parent, keep, keep + T, P)
+            pause()
+            wp.wp_pages_copy(k, v, copies)
+            pause()
+            slot = (keep[:, None] + node).flatten()
+            qr = wp.wp_rope_append(q, kn, vn, k, v, slot, seq, slot, 1e4, wp.ROPE_HALF_SPLIT, block_table=table)
+            pause()
+            o, lse = wp.wp_decode_tree(qr.view(B, T, Hq, d), k, v, keep, parents, block_table=table, group_cut=[50, 7, 2 ** 31 - 1, 200])
+            pause()
+            n_keep = 1 + (rows + i) % path.shape[1]
+            lens = wp.wp_kv_compact(k, v, keep, path, n_keep, block_table=table)
+            pause()
+            back, _ = wp.wp_rope_qk(qr.view(B, T, Hq, d), None, 1e4, wp.ROPE_HALF_SPLIT, pos=slot.view(B, T), inverse=True)
+            outs += [o, lse, lens, info, back]
+        torch.cuda.synchronize()
+        return outs + [k, v, refs, table]
+
+    one, many = steps(True), steps(False)
+    assert all(int(i[0]) == wp.PAGES_OK for i in one[3:-4:5])
+    for x, y in zip(one, many):
+        assert torch.equal(x, y)
+    assert torch.isfinite(one[0].float()).all() and wp.wp_device_status() == 0
