@@ -737,10 +737,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         const float l0 = sum4(all_part), l1 = sum4(all_part + 4 * NR), l = l0 * f0 + l1 * f1;
         const bool live = node < plan.n;
         // a stream without a visible key adds nothing, whatever its accumulator
-        // holds; rows of nodes that are not there are 0, a spoilt segment's NaN
-        const float inv = spoilt ? __int_as_float(0x7FC00000) : live && l != 0.f ? 1.f / l : 0.f;
-        all_alpha[r] = l0 == 0.f && !spoilt ? 0.f : f0 * inv;
-        all_alpha[NR + r] = l1 == 0.f && !spoilt ? 0.f : f1 * inv;
+        // holds; rows of nodes that are not there are 0, chosen and not multiplied
+        // to it: their q may be anything, and so may the factors be. A spoilt
+        // segment's rows are NaN.
+        const float inv = spoilt ? __int_as_float(0x7FC00000) : l != 0.f ? 1.f / l : 0.f;
+        all_alpha[r] = !spoilt && (!live || l0 == 0.f) ? 0.f : f0 * inv;
+        all_alpha[NR + r] = !spoilt && (!live || l1 == 0.f) ? 0.f : f1 * inv;
         if (seg.slot >= 0)
           a.lse_part[static_cast<int64_t>(seg.slot) * rows + r] = spoilt ? INFINITY : m + __log2f(l);
         else if (a.lse != nullptr)
