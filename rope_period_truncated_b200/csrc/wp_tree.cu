@@ -396,7 +396,11 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     const uint32_t o_addr = lane_addr + COL_O;
     const float c2 = a.scale_log2;
     const uint64_t c2x2 = pack_f2(c2, c2);
-    float m_run = LOWEST, l_run = 0.f;  // base-2 units
+    // A lane without a row, or with the row of a node that is not there, has no
+    // say in when the warp moves its maxima: the products read shared memory
+    // behind Q for the one, a q that may be anything for the other, and a present
+    // row's roundings must not depend on either. No logit exceeds infinity.
+    float m_run = my_sees != 0 && r < rows ? LOWEST : INFINITY, l_run = 0.f;  // base-2 units
     int bnd_cnt = 0;
     bool ok = nsub > 0;
     for (int u = 0; ok && u < nsub; ++u) {

@@ -50,3 +50,32 @@ def test_absent_nodes_are_zero(d, Hq, Hkv, T, lens, nodes, P, kind):
         assert (o[b, n:] == 0).all() and (lse[b, :, n:] == -INF).all(), f"sequence {b}"
         assert torch.isfinite(o[b, :n].float()).all() and torch.isfinite(lse[b, :, :n]).all(), f"sequence {b}"
     assert wp.wp_device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["one", "all", "large", "nan"])
+@pytest.mark.parametrize("d,Hq,Hkv,T,lens,nodes,P", [c for c in ABSENT if c[3] * c[1] // c[2] > 32])
+def test_absent_nodes_change_nothing(d, Hq, Hkv, T, lens, nodes, P, kind):
+    """The rows that are there come out to the bit as with zeros in the unused q."""
+    c = Case(d + T, d, Hq, Hkv, T, lens, nodes, P, False)
+    cut = [40, 2 ** 31 - 1, 300, 70] * (d // 64)
+    _unused(c, "zeros")
+    want, wlse = c.run(cut)
+    _unused(c, kind)
+    o, lse = c.run(cut)
+    assert torch.equal(o, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,T", [(128, 8, 2, 21), (64, 4, 1, 10), (128, 8, 2, 9), (64, 3, 1, 43), (128, 8, 2, 5), (64, 3, 1, 7)])
+def test_tree_whatever_shared_memory_held(d, Hq, Hkv, T):
+    """Row counts that do not fill a warp: the lanes without a row have no say, so a call repeats to the bit whatever the
+    calls before it left in shared memory."""
+    c = Case(d + T, d, Hq, Hkv, T, [1500, 2300], [T, T], 16, False)
+    wide = wp.TREE_MAX_NODES // (Hq // Hkv)  # another row count: its q, k and v lie elsewhere
+    before = [Case(7, d, Hq, Hkv, n, [2048, 2048], [n, n], 0, gm, scale=scale)
+              for scale in (0.0, 30.0) for n, gm in ((T, False), (T, True), (wide, False))]
+    got = []
+    for x in before:
+        x.run(None)
+        got.append(c.run(None))
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
