@@ -479,6 +479,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (lane == 0) mbar_arrive(&t_ready[seg.index % TABLES]);
       }
       ok = warp_wait(q_full, seg.index & 1, lim, abort_flag);
+      if (ok && seg.plan.n < a.T) {
+        // The q of nodes that are not there may be anything, and its logits would
+        // take part in the votes on the maxima: zeros instead.
+        const int first = seg.plan.n * R, pieces = (rows - first) * 2;  // 16-byte pieces per group
+        for (int e = lane; e < pieces * G; e += 32)
+          *reinterpret_cast<uint4 *>(smem + lay.q_off + (e / pieces) * L::Q_TILE + first * 32 + (e % pieces) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_shared();
+        __syncwarp();
+      }
       for (int u = 0; ok && u < seg.tiles; ++u, ++it) {
         const int hh = it & 1;
         const uint32_t cls = tile_classes<TILE>(my_cut, G, seg.plan.len, deepest, seg.k_begin + u * TILE, lane);
