@@ -347,7 +347,11 @@ __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const __grid_c
     const int before = i == 0 ? -1 : a.path[static_cast<int64_t>(b) * a.A + i - 1];
     if (bad || i >= n) break;
     const int64_t from = static_cast<int64_t>(len) + p;
-    if (p <= before || from >= cache_capacity(g)) {
+    // p >= i follows from a whole path that increases from 0 or more, but each
+    // thread sees two entries of it: without this, an entry before a bad one
+    // elsewhere could lead it to a key below 0 or a target behind the capacity,
+    // and to a page looked up outside the block table.
+    if (p < i || p <= before || from >= cache_capacity(g)) {
       bad = true;
       break;
     }

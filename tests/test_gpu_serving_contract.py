@@ -79,3 +79,23 @@ def test_tree_whatever_shared_memory_held(d, Hq, Hkv, T):
         got.append(c.run(None))
     for o, lse in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("gm", [False, True])
+@pytest.mark.parametrize("P", [0, 16])
+def test_compaction_of_paths_that_leave_the_cache(P, gm):
+    """Paths that increase from entry to entry in places, and lead below key 0 or behind the capacity there: refused whole,
+    also in the last row of the block table, whose neighbours are other memory."""
+    cap, B = 64, 4
+    low = -2 ** 31
+    paths = [[0, -1000000, -999999, -999998, 5, 6], [0, low, low + 1, 0, 1, 2], [3, 4, 0, 1, 2, 3], [0, -5, -4, -3, -2, -1]]
+    lens = [10, 40, 60, 59]  # with 60 + 4 and 59 + 5 at the capacity
+    n = B * cap // P if P else B
+    v = torch.randn(n, 2, P or cap, 64, device="cuda").to(torch.bfloat16)
+    k = torch.randn(*((n, 2, 4, P or cap, 16) if gm else (n, 2, P or cap, 64)), device="cuda").to(torch.bfloat16)
+    k0, v0 = k.clone(), v.clone()
+    table = torch.arange(n, dtype=torch.int32, device="cuda").view(B, -1) if P else None
+    out = wp.wp_kv_compact(k, v, _i32(lens), _i32(paths), _i32([6] * B), block_table=table)
+    assert out.tolist() == [-1] * B and torch.equal(k, k0) and torch.equal(v, v0)
+    out = wp.wp_kv_compact(k, v, _i32([58] * B), _i32([[0, 1, 2, 3, 4, 5]] * B), _i32([6] * B), block_table=table)  # up to the last key
+    assert out.tolist() == [64] * B and torch.equal(k, k0) and torch.equal(v, v0)
