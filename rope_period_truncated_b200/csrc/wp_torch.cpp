@@ -130,8 +130,10 @@ wp_rows rows(const at::Tensor &t) {
 }
 
 // Device and stream of a call: the given stream, or the current one of the
-// tensors' device. What a call allocates is marked as used on a stream that is
-// not the current one.
+// tensors' device. What a call allocates is written on its stream, so it comes
+// from that stream's memory: memory that the current stream has given back may
+// still be read by what is enqueued there. Results are marked as used on the
+// current stream too, where the caller goes on with them.
 struct Call {
   c10::cuda::CUDAGuard guard;
   int device;
@@ -156,9 +158,12 @@ struct Call {
     stream = c10::cuda::CUDAStream::unpack3(attr("stream_id"), static_cast<c10::DeviceIndex>(index),
                                             static_cast<c10::DeviceType>(attr("device_type")));
   }
-  at::Tensor empty(at::IntArrayRef size, at::ScalarType type) {
-    at::Tensor t = at::detail::empty_cuda(size, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)), std::nullopt);
-    if (stream != current) t.record_stream(stream);
+  at::Tensor empty(at::IntArrayRef size, at::ScalarType type, bool result = true) {
+    const c10::Device on(c10::kCUDA, static_cast<c10::DeviceIndex>(device));
+    if (stream == current) return at::detail::empty_cuda(size, type, on, std::nullopt);
+    const c10::cuda::CUDAStreamGuard its(stream);
+    at::Tensor t = at::detail::empty_cuda(size, type, on, std::nullopt);
+    if (result) t.record_stream(current);
     return t;
   }
   void *handle() const { return stream.stream(); }
@@ -354,7 +359,7 @@ struct Workspace {
       data = t.data_ptr();
       bytes = t.nbytes();
     } else if (need > 0) {
-      made = call.empty({static_cast<int64_t>(need)}, at::kByte);
+      made = call.empty({static_cast<int64_t>(need)}, at::kByte, false);
       data = made.data_ptr();
       bytes = need;
     }

@@ -9,7 +9,10 @@ contiguous V [B,Hkv,Lmax,d] with K the same (rows) or [B,Hkv,d/16,Lmax,16]
 (group-major); paged V [n_pages,Hkv,P,d] with K the same or
 [n_pages,Hkv,d/16,P,16] and ``block_table`` int32 [B,max_pages] (device).
 
-Calls run on ``stream``, or on the current stream of the tensors' device.
+Calls run on ``stream``, or on the current stream of the tensors' device. With
+a ``stream``, the caller lets it wait for what makes the inputs, keeps the
+inputs until it has read them, and waits for it before using the results, which
+are allocated on ``stream`` and may be used and dropped on the current one.
 """
 from __future__ import annotations
 

@@ -99,3 +99,47 @@ def test_compaction_of_paths_that_leave_the_cache(P, gm):
     assert out.tolist() == [-1] * B and torch.equal(k, k0) and torch.equal(v, v0)
     out = wp.wp_kv_compact(k, v, _i32([58] * B), _i32([[0, 1, 2, 3, 4, 5]] * B), _i32([6] * B), block_table=table)  # up to the last key
     assert out.tolist() == [64] * B and torch.equal(k, k0) and torch.equal(v, v0)
+
+
+def _bf16(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+
+
+def test_results_on_another_stream_take_no_memory_still_in_use():
+    """A call on a stream of its own, while the current stream has yet to read memory that it has given back; and the other
+    way round, a call's result given back while the current stream has yet to read it."""
+    shape = (1, 4096, 8, 128)
+    x, q, r = _bf16(1, *shape), _bf16(2, *shape), _bf16(3, *shape)
+    want_x, want_q = x.clone(), wp.wp_rope_qk(q, None, 1e4, wp.ROPE_HALF_SPLIT)[0]
+    y, z, side = torch.empty_like(x), torch.empty_like(x), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    y.copy_(x)
+    del x
+    o, _ = wp.wp_rope_qk(q, None, 1e4, wp.ROPE_HALF_SPLIT, stream=side)  # does not wait for the current stream
+    torch.cuda.synchronize()
+    assert torch.equal(y, want_x) and torch.equal(o, want_q)
+    torch.cuda._sleep(200_000_000)
+    z.copy_(o)
+    del o
+    o, _ = wp.wp_rope_qk(r, None, 1e4, wp.ROPE_HALF_SPLIT, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(z, want_q) and torch.equal(o, wp.wp_rope_qk(r, None, 1e4, wp.ROPE_HALF_SPLIT)[0])
+
+
+def test_given_stream_of_a_captured_fork():
+    """Inside a capture, calls on a stream that was forked into it: outputs and workspace are the graph's own."""
+    c = Case(3, 128, 8, 2, 8, [3000, 900], [8, 6], 64, True)
+    args, nodes = c.args(), _i32(c.nodes)
+    want = wp.wp_decode_tree(*args, n_nodes=nodes, block_table=c.table)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        o, lse = wp.wp_decode_tree(*args, n_nodes=nodes, block_table=c.table, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        o.zero_()
+        graph.replay()
+        other = wp.wp_decode_tree(*args, n_nodes=nodes, block_table=c.table)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(other[0], want[0])
