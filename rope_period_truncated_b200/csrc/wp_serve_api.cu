@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <utility>
 
 #include "waveprune.h"
 #include "wp_serve.h"
@@ -77,7 +78,14 @@ bool may_overlap(const wp_rows *x, int Hx, const Extent &ex, const wp_rows *y, i
   const int64_t at = (static_cast<int64_t>(ey.lo) - static_cast<int64_t>(ex.lo)) / 2;  // y relative to x
   const bool apart = at >= in_x || -at >= in_y;
   const int64_t span = std::max(in_x, at + in_y) - std::min<int64_t>(0, at);  // both, within one token
-  const bool fits = (B == 1 || x->stride_b >= span) && (N == 1 || x->stride_n >= span);
+  // from token to token at least the span, from run to run of tokens at least a whole run
+  struct {
+    int64_t stride;
+    int size;
+  } in = {x->stride_n, N}, out = {x->stride_b, B};
+  if (N == 1 || (B > 1 && in.stride > out.stride)) std::swap(in, out);
+  const int64_t run = span + (in.size > 1 ? in.stride * (in.size - 1) : 0);
+  const bool fits = (in.size == 1 || in.stride >= span) && (out.size == 1 || out.stride >= run);
   return !(apart && fits);
 }
 
