@@ -478,7 +478,7 @@ typedef struct {
  *                H_k = 0 leaves that side out (its pointers are not read).
  *                An output may be its own input (same base and strides,
  *                except WP_ROPE_HALF_SPLIT_PAIRED); any other overlap of an
- *                output with an input or output is WP_ERR_ARG. Inputs may be
+ *                output with an input (pos too) or output is WP_ERR_ARG. Inputs may be
  *                broadcast (stride 0), outputs may not.
  *   rot_dim      the first rot_dim dims of each head rotate (a multiple of
  *                16, 16..d_h), the others are copied; f_c = theta^(-2c/rot_dim).
@@ -519,7 +519,8 @@ int wp_rope_qk(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_rows *k
  *                keys, as in wp_decode_paged (Lmax is ignored).
  *   rotation     as in wp_rope_qk; q_out and the cache take the layout's
  *                output order. q_out may be q (not with the paired layout);
- *                the caches overlap nothing.
+ *                it and the caches overlap nothing else, the index arrays and
+ *                the block table included (WP_ERR_ARG).
  * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
  */
 int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_rows *k, const wp_rows *v, int H_kv, int T,

@@ -221,6 +221,10 @@ int wp_rope_qk(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_rows *k
       }
     }
   if (H_q > 0 && H_k > 0 && may_overlap(q_out, H_q, eo[0], k_out, H_k, eo[1], B, N, d_h)) return WP_ERR_ARG;
+  // positions are read by blocks that start after others have stored
+  const Extent positions = extent(pos, static_cast<size_t>(B) * N * 4);
+  for (int i = 0; i < 2; ++i)
+    if (H[i] > 0 && meets(positions, eo[i])) return WP_ERR_ARG;
   RotaryArgs a;
   std::memset(&a, 0, sizeof(a));
   if (H_q > 0) a.q = rows_arg(q), a.q_out = rows_arg(q_out);
@@ -256,8 +260,14 @@ int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_row
   if (!rows_ok(k, 1, T, H_kv, d_h, false, &ek) || !rows_ok(v, 1, T, H_kv, d_h, false, &ev)) return WP_ERR_ARG;
   const Extent cache[2] = {pool_extent(a.cache, kcache), pool_extent(a.cache, vcache)};
   if (meets(cache[0], cache[1])) return WP_ERR_ARG;
-  for (const Extent &c : cache)
+  // read by blocks that start after others have stored
+  const size_t nt = static_cast<size_t>(T) * 4;
+  const Extent index[4] = {extent(pos, nt), extent(seq, nt), extent(slot, nt), extent(block_table, static_cast<size_t>(B) * max_pages * 4)};
+  for (const Extent &c : cache) {
     if (meets(ek, c) || meets(ev, c)) return WP_ERR_ARG;
+    for (const Extent &i : index)
+      if (meets(i, c)) return WP_ERR_ARG;
+  }
   if (H_q > 0) {
     if (!rows_ok(q, 1, T, H_q, d_h, false, &eq) || !rows_ok(q_out, 1, T, H_q, d_h, true, &eo)) return WP_ERR_ARG;
     if (same_rows(q, q_out, 1, T, H_q)) {
@@ -269,6 +279,8 @@ int wp_rope_append(const wp_rows *q, const wp_rows *q_out, int H_q, const wp_row
       return WP_ERR_ARG;
     for (const Extent &c : cache)
       if (meets(eq, c) || meets(eo, c)) return WP_ERR_ARG;
+    for (const Extent &i : index)
+      if (meets(i, eo)) return WP_ERR_ARG;
     a.q = rows_arg(q), a.q_out = rows_arg(q_out);
   }
   a.k = rows_arg(k);

@@ -45,3 +45,39 @@ def test_tensors_that_meet_across_tokens_are_refused(lib, swap):
                 _accepted(lib.wp_rope_qk, args)
             else:
                 assert lib.wp_rope_qk(*args) == code
+
+
+# ------------------------------------------------------ index arrays and outputs
+
+def test_index_arrays_inside_what_is_written_are_refused(lib):
+    """Positions, sequences, slots and block table against the outputs and the caches, first and last element."""
+    B, N, Hq, Hk, d = 2, 5, 4, 2, 64
+    at = [FAKE + i * M for i in range(16)]
+    q, qo = rows(at[0], N * Hq * d, Hq * d, d), rows(at[1], N * Hq * d, Hq * d, d)
+    k, ko = rows(at[2], N * Hk * d, Hk * d, d), rows(at[3], N * Hk * d, Hk * d, d)
+    good = [q, qo, Hq, k, ko, Hk, B, N, d, d, at[4], 0, 1e4, None, 1.0, 1.0, 0, 0, None]
+    _expect(lib.wp_rope_qk, good, [
+        ({10: at[1]}, ARG, "pos over q's output"), ({10: at[1] + B * N * Hq * d * 2 - 4}, ARG, "pos over its last element"),
+        ({10: at[3] - B * N * 4 + 4}, ARG, "pos runs into k's output"), ({10: at[3] + B * N * Hk * d * 2 - 4}, ARG, "pos in k's output"),
+        ({10: at[0], 1: q}, ARG, "pos in q rotated in place")])
+    _accepted(lib.wp_rope_qk, good)
+    _accepted(lib.wp_rope_qk, [{10: at[1] + B * N * Hq * d * 2}.get(i, x) for i, x in enumerate(good)])  # right behind
+    _accepted(lib.wp_rope_qk, [{10: at[0]}.get(i, x) for i, x in enumerate(good)])  # in an input that nobody writes
+    T, Lmax, P, MP, n = 6, 100, 16, 8, 20
+    q, qo, k, v = (rows(at[i], 0, H * d, d) for i, H in enumerate((Hq, Hq, Hk, Hk)))
+    pos, seq, slot, table, kc, vc = at[4:10]
+    good = [q, qo, Hq, k, v, Hk, T, d, d, pos, seq, slot, kc, 0, vc, B, Lmax, None, 0, 0, 0, 1e4, None, 1.0, 1.0, 0, None]
+    paged = {17: table, 18: MP, 19: P, 20: n}
+    bytes_of = {"contiguous": B * Hk * Lmax * d * 2, "paged": n * Hk * P * d * 2}
+    bad = []
+    for name, i in (("pos", 9), ("seq", 10), ("slot", 11)):
+        for where, first, size in (("q's output", at[1], T * Hq * d * 2), ("K", kc, bytes_of["contiguous"]), ("V", vc, bytes_of["contiguous"])):
+            bad += [({i: first}, ARG, f"{name} over {where}"), ({i: first + size - 4}, ARG, f"{name} over the end of {where}"),
+                    ({i: first - 4 * T + 4}, ARG, f"{name} runs into {where}")]
+    for first, size in ((at[1], T * Hq * d * 2), (kc, bytes_of["paged"]), (vc, bytes_of["paged"])):
+        bad += [({**paged, 17: first}, ARG, "block table over it"), ({**paged, 17: first + size - 4}, ARG, "block table over its end"),
+                ({**paged, 17: first - B * MP * 4 + 4}, ARG, "block table runs into it")]
+    _expect(lib.wp_rope_append, good, bad)
+    _accepted(lib.wp_rope_append, good)
+    _accepted(lib.wp_rope_append, [paged.get(i, x) for i, x in enumerate(good)])
+    _accepted(lib.wp_rope_append, [{9: pos, 10: seq, 11: pos}.get(i, x) for i, x in enumerate(good)])  # one array for both
