@@ -628,7 +628,7 @@ size_t wp_pages_update_workspace_bytes(int B, int n_pages);
  * workspace (8-byte aligned; contents on entry do not matter; calls that may run
  * at the same time need workspaces of their own).
  * Errors: WP_ERR_ARG, WP_ERR_UNSUPPORTED (capacity or n_pages above 2^30, B
- * above 65535), WP_ERR_CUDA.
+ * above 65535, more than 2^31-1 block table entries), WP_ERR_CUDA.
  */
 int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32_t *lens, const int32_t *parent,
                     const int32_t *keep, const int32_t *new_lens, int32_t *refs_out, int32_t *block_table_out,

@@ -425,6 +425,8 @@ int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32
     if (p == nullptr || !aligned(p, p == workspace ? 8 : 4)) return WP_ERR_ARG;
   if (B <= 0 || max_pages <= 0 || page_size < 16 || page_size % 16 != 0 || n_pages <= 0) return WP_ERR_ARG;
   if (static_cast<int64_t>(max_pages) * page_size > (1ll << 30) || B > 65535 || n_pages > (1 << 30)) return WP_ERR_UNSUPPORTED;
+  // the pages that all rows need, and a page's drops and takes, are counted in 32 bits
+  if (static_cast<int64_t>(B) * max_pages > 0x7fffffff) return WP_ERR_UNSUPPORTED;
   if (ws_bytes < wp_pages_update_workspace_bytes(B, n_pages)) return WP_ERR_ARG;
   // the outputs are written while the inputs are still read
   const size_t nb = static_cast<size_t>(B) * 4, nt = nb * max_pages, np = static_cast<size_t>(n_pages) * 4;

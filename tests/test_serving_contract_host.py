@@ -81,3 +81,17 @@ def test_index_arrays_inside_what_is_written_are_refused(lib):
     _accepted(lib.wp_rope_append, good)
     _accepted(lib.wp_rope_append, [paged.get(i, x) for i, x in enumerate(good)])
     _accepted(lib.wp_rope_append, [{9: pos, 10: seq, 11: pos}.get(i, x) for i, x in enumerate(good)])  # one array for both
+
+
+# -------------------------------------------------------- sizes beyond 32 bits
+
+def test_a_block_table_beyond_32_bits_is_refused(lib):
+    """The pages that all rows need together stay within 32 bits: a table of 2^31 entries or more is not taken, one of
+    2^31 - 32 is."""
+    at = [FAKE + (i << 40) for i in range(12)]
+    n = 100
+    call = lambda B, MP: lib.wp_pages_update(*at[:11], B, MP, 16, n, at[11], lib.wp_pages_update_workspace_bytes(B, n), None)  # noqa: E731
+    for B, MP in ((32, 1 << 26), (65535, 1 << 26), (65535, 32769), (1 << 15, 1 << 16)):
+        assert call(B, MP) == UNSUPPORTED
+    if not torch.cuda.is_available():
+        assert call(32, (1 << 26) - 1) == wp.WP_ERR_CUDA and call(65535, 32768) == wp.WP_ERR_CUDA
