@@ -623,7 +623,7 @@ size_t wp_pages_update_workspace_bytes(int B, int n_pages);
  *   info         device int32 out [4]: WP_PAGES_*, pages taken (or that would
  *                have been), free pages there were, copies.
  * If the free pages do not suffice (WP_PAGES_SHORT) or an entry is out of
- * range (WP_PAGES_BAD_ARGUMENT), nothing changes: the outputs are the inputs
+ * range (WP_PAGES_BAD_ARGUMENT; also a count that would be), nothing changes: the outputs are the inputs
  * and copies is empty. No output overlaps an input, another output or the
  * workspace (8-byte aligned; contents on entry do not matter; calls that may run
  * at the same time need workspaces of their own).

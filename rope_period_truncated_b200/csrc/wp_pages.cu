@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
   int32_t *held_refs = own ? copying + a.B : nullptr;
   const int32_t *refs = own ? held_refs : a.refs;
   __shared__ int warp_sums[33];
-  __shared__ int s_bad, s_lost, s_free, s_below, s_copies;
+  __shared__ int s_bad, s_lost, s_free, s_out, s_copies;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), blocks = static_cast<int>(cluster.num_blocks());
   const int tid = rank * PG_THREADS + threadIdx.x;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
   const int P = a.page_size, MP = a.max_pages;
   const int64_t cap = static_cast<int64_t>(MP) * P;
   const int warp = tid / 32, lane = tid % 32, warps = NT / 32;  // a warp takes a row of the tables
-  if (threadIdx.x == 0) s_bad = s_lost = s_free = s_below = s_copies = 0;
+  if (threadIdx.x == 0) s_bad = s_lost = s_free = s_out = s_copies = 0;
   __syncthreads();
 
   // 1. The counts to work on, and the rows' arguments.
@@ -178,7 +178,9 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
     const int r = refs[i];
     const unsigned long long c = counts[i];
     mine += holders(r, c) == 0;
-    if ((c & 0xffffffffu) > static_cast<unsigned>(r)) s_below = 1;
+    // more drops than holders, or more holders than 32 bits hold (a page that the caller has pinned by a huge count)
+    const unsigned drops = static_cast<unsigned>(c & 0xffffffffu), takes = static_cast<unsigned>(c >> 32);
+    if (drops > static_cast<unsigned>(r) || takes > static_cast<unsigned>(INT_MAX) - static_cast<unsigned>(r) + drops) s_out = 1;
   }
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) atomicAdd(&s_free, mine);
@@ -204,7 +206,7 @@ __global__ void __launch_bounds__(PG_THREADS) pages_update_kernel(const __grid_c
     }
   cluster.sync();
   const int theirs = of_blocks(&s_free);
-  bad = __any_sync(0xffffffffu, of_blocks(&s_below)) || bad;
+  bad = __any_sync(0xffffffffu, of_blocks(&s_out)) || bad;
   const int free_before = __reduce_add_sync(0xffffffffu, lane < rank ? theirs : 0);
   const int free_all = __reduce_add_sync(0xffffffffu, theirs);
   const bool refused = bad || total > free_all;

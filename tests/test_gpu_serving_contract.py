@@ -143,3 +143,24 @@ def test_given_stream_of_a_captured_fork():
         graph.replay()
         other = wp.wp_decode_tree(*args, n_nodes=nodes, block_table=c.table)
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and torch.equal(other[0], want[0])
+
+
+@pytest.mark.parametrize("pool", [6, 9000])
+def test_pages_with_counts_near_32_bits(pool):
+    """A page that the caller has pinned by the largest count can be kept and given up; one more holder is refused whole."""
+    top, P = 2 ** 31 - 1, 16
+    refs, table, lens = [0] * pool, [[0, -1], [1, -1]], [16, 16]
+    refs[0], refs[1] = top, 1
+
+    def update(refs, parent, keep, new):
+        return [t.tolist() for t in wp.wp_pages_update(*(_i32(x) for x in (refs, table, lens, parent, keep, new)), P)]
+
+    one = update(refs, [0, 1], [16, 16], [20, 16])
+    assert one[0][:3] == [top, 1, 1] and one[1] == [[0, 2], [1, -1]] and one[4][0] == wp.PAGES_OK
+    gone = update(refs, [0, 1], [0, 16], [0, 16])
+    assert gone[0][:2] == [top - 1, 1] and gone[4][0] == wp.PAGES_OK
+    fork = update(refs, [0, 0], [16, 16], [16, 16])
+    assert fork == [refs, table, lens, [[-1, -1, 0]] * 2, [wp.PAGES_BAD_ARGUMENT, 0, 0, 0]]
+    less = [top - 1] + refs[1:]
+    fork = update(less, [0, 0], [16, 16], [16, 16])
+    assert fork[0][:2] == [top, 0] and fork[1] == [[0, -1], [0, -1]] and fork[4][0] == wp.PAGES_OK
