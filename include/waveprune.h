@@ -642,7 +642,7 @@ int wp_pages_update(const int32_t *refs, const int32_t *block_table, const int32
  * head. An entry with a page outside the pool, rows outside 1..page_size, or
  * source = target copies nothing. A target page must not appear in another
  * entry; the pools and copies do not overlap. Errors: WP_ERR_ARG,
- * WP_ERR_UNSUPPORTED, WP_ERR_CUDA.
+ * WP_ERR_UNSUPPORTED (also: page_size * d_h above 2^33), WP_ERR_CUDA.
  */
 int wp_pages_copy(void *k_pages, int k_layout, void *v_pages, const int32_t *copies, int n, int n_pages, int page_size,
                   int H_kv, int d_h, void *stream);

@@ -468,6 +468,7 @@ int wp_pages_copy(void *k_pages, int k_layout, void *v_pages, const int32_t *cop
   // any non-null block table: the pools are paged, the copies name their pages
   const int rc = cache_args(k_pages, k_layout, v_pages, 1, 0, copies, 1, page_size, n_pages, H_kv, d_h, &a.cache);
   if (rc != WP_OK) return rc;
+  if (static_cast<int64_t>(page_size) * (d_h / 8) > (1ll << 30)) return WP_ERR_UNSUPPORTED;  // 16-byte pieces of a head's page, in 32 bits
   const Extent k = pool_extent(a.cache, k_pages), v = pool_extent(a.cache, v_pages), c = extent(copies, static_cast<size_t>(n) * 12);
   if (meets(k, v) || meets(k, c) || meets(v, c)) return WP_ERR_ARG;
   a.copies = copies;

@@ -95,3 +95,12 @@ def test_a_block_table_beyond_32_bits_is_refused(lib):
         assert call(B, MP) == UNSUPPORTED
     if not torch.cuda.is_available():
         assert call(32, (1 << 26) - 1) == wp.WP_ERR_CUDA and call(65535, 32768) == wp.WP_ERR_CUDA
+
+
+def test_page_copies_beyond_32_bits_are_refused(lib):
+    """The pieces of a page are counted in 32 bits: pages of 2^27 rows of 128 would have copied nothing."""
+    call = lambda P, d: lib.wp_pages_copy(FAKE, 0, FAKE + (1 << 50), FAKE + (1 << 52), 4, 2, P, 1, d, None)  # noqa: E731
+    for P, d in ((1 << 27, 128), (1 << 28, 64), ((1 << 26) + 16, 128), (1 << 30, 64)):
+        assert call(P, d) == UNSUPPORTED
+    if not torch.cuda.is_available():
+        assert call(1 << 26, 128) == call(1 << 27, 64) == wp.WP_ERR_CUDA
