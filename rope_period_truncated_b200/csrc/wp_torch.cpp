@@ -69,6 +69,12 @@ T *ptr(const at::Tensor &t) {
 }
 const int32_t *ints(const at::Tensor &t) { return ptr<int32_t>(t); }
 
+// A size for the C ABI.
+int fit(int64_t n) {
+  if (n > INT_MAX) value_error("a size does not fit 32 bits: " + std::to_string(n));
+  return static_cast<int>(n);
+}
+
 double number(PyObject *o) {
   const double x = PyFloat_AsDouble(o);
   if (x == -1.0 && PyErr_Occurred()) throw python_error();
@@ -209,27 +215,25 @@ Cache cache(PyObject *ko, PyObject *vo, PyObject *bt, int device, int64_t B = -1
     value_error("K cache shape mismatch");
   }
   if ((Hkv >= 0 && H != Hkv) || (d >= 0 && dd != d)) value_error("the cache's heads or head dim do not match");
-  for (int64_t x : {n, H, rows, dd})
-    if (x > INT_MAX) value_error("a size of the cache does not fit 32 bits");
   Cache c;
   c.k = k.data_ptr();
   c.v = v.data_ptr();
   c.layout = gm ? WP_KCACHE_GROUP_MAJOR : WP_KCACHE_ROWS;
-  c.Hkv = static_cast<int>(H);
-  c.d = static_cast<int>(dd);
+  c.Hkv = fit(H);
+  c.d = fit(dd);
   if (bt == Py_None) {
     if (B >= 0 && n != B) value_error("the cache holds " + std::to_string(n) + " sequences, expected " + std::to_string(B));
-    c.B = static_cast<int>(n);
-    c.Lmax = static_cast<int>(rows);
+    c.B = fit(n);
+    c.Lmax = fit(rows);
     return c;
   }
   const at::Tensor &t = tensor(bt, "block_table", I32, 2, device);
   if (B >= 0 && t.size(0) != B) value_error("the block table has " + std::to_string(t.size(0)) + " rows, expected " + std::to_string(B));
   c.block_table = ints(t);
-  c.B = static_cast<int>(t.size(0));
-  c.max_pages = static_cast<int>(t.size(1));
-  c.page_size = static_cast<int>(rows);
-  c.n_pages = static_cast<int>(n);
+  c.B = fit(t.size(0));
+  c.max_pages = fit(t.size(1));
+  c.page_size = fit(rows);
+  c.n_pages = fit(n);
   return c;
 }
 
@@ -246,7 +250,7 @@ PyObject *rope_qk(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const char *names[2] = {"q", "k"}, *out_names[2] = {"out_q", "out_k"};
   const at::Tensor &x = tensor(has[0] ? a[0] : a[1], has[0] ? "q" : "k", BF16, 4, -1, false);
   const int device = x.get_device();
-  const int64_t B = x.size(0), N = x.size(1), d = x.size(3);
+  const int B = fit(x.size(0)), N = fit(x.size(1)), d = fit(x.size(3));
   Call call(device, a[13]);
   wp_rows in[2] = {}, out[2] = {};
   int H[2] = {0, 0};
@@ -259,6 +263,7 @@ PyObject *rope_qk(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     const at::Tensor &t = tensor(a[i], names[i], BF16, 4, device, false);
     if (t.size(0) != B || t.size(1) != N || t.size(3) != d) value_error("q/k shape mismatch");
+    H[i] = fit(t.size(2));
     if (o != Py_None) {
       const at::Tensor &given = tensor(o, out_names[i], BF16, 4, device, false);
       if (given.sizes() != t.sizes()) value_error(std::string(out_names[i]) + " shape mismatch");
@@ -268,7 +273,6 @@ PyObject *rope_qk(PyObject *, PyObject *const *a, Py_ssize_t n) {
       out[i] = rows(made[i]);
     }
     in[i] = rows(t);
-    H[i] = static_cast<int>(t.size(2));
   }
   const int32_t *pos = nullptr;
   if (a[4] != Py_None) {
@@ -278,14 +282,13 @@ PyObject *rope_qk(PyObject *, PyObject *const *a, Py_ssize_t n) {
   }
   const double theta = number(a[2]), scale_all = number(a[8]), amplitude = number(a[9]);
   const int layout = integer(a[3], "layout"), pos0 = integer(a[5], "pos0");
-  const int rot = a[6] == Py_None ? static_cast<int>(d) : integer(a[6], "rot_dim");
+  const int rot = a[6] == Py_None ? d : integer(a[6], "rot_dim");
   const std::vector<double> fs = frequencies(a[7], rot);
   const int inverse = PyObject_IsTrue(a[10]);
   if (inverse < 0) throw python_error();
-  if (B > INT_MAX || N > INT_MAX) value_error("too many tokens");
   run("wp_rope_qk", [&] {
-    return f_rope_qk(&in[0], &out[0], H[0], &in[1], &out[1], H[1], static_cast<int>(B), static_cast<int>(N), static_cast<int>(d), rot, pos,
-                     pos0, theta, data(fs), scale_all, amplitude, layout, inverse, call.handle());
+    return f_rope_qk(&in[0], &out[0], H[0], &in[1], &out[1], H[1], B, N, d, rot, pos, pos0, theta, data(fs), scale_all, amplitude, layout,
+                     inverse, call.handle());
   });
   PyObject *r = PyTuple_New(2);
   for (int i = 0; i < 2; ++i) PyTuple_SET_ITEM(r, i, has[i] ? give(a[11 + i], made[i]) : Py_NewRef(Py_None));
@@ -299,7 +302,7 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   count(n, 17);
   const at::Tensor &k = tensor(a[1], "k", BF16, 3, -1, false);
   const int device = k.get_device();
-  const int64_t T = k.size(0), Hkv = k.size(1), d = k.size(2);
+  const int T = fit(k.size(0)), Hkv = fit(k.size(1)), d = fit(k.size(2));
   const at::Tensor &v = tensor(a[2], "v", BF16, 3, device, false);
   if (v.sizes() != k.sizes()) value_error("k/v shape mismatch");
   const int32_t *index[3];
@@ -312,7 +315,7 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const Cache c = cache(a[3], a[4], a[10], device, -1, Hkv, d);
   const double theta = number(a[8]), scale_all = number(a[13]), amplitude = number(a[14]);
   const int layout = integer(a[9], "layout");
-  const int rot = a[11] == Py_None ? static_cast<int>(d) : integer(a[11], "rot_dim");
+  const int rot = a[11] == Py_None ? d : integer(a[11], "rot_dim");
   const std::vector<double> fs = frequencies(a[12], rot);
   Call call(device, a[16]);
   wp_rows q = {}, qo = {};
@@ -321,6 +324,7 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
   if (a[0] != Py_None) {
     const at::Tensor &t = tensor(a[0], "q", BF16, 3, device, false);
     if (t.size(0) != T || t.size(2) != d) value_error("q shape mismatch");
+    Hq = fit(t.size(1));
     if (a[15] != Py_None) {
       const at::Tensor &given = tensor(a[15], "out_q", BF16, 3, device, false);
       if (given.sizes() != t.sizes()) value_error("out_q shape mismatch");
@@ -330,16 +334,13 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
       qo = rows(made);
     }
     q = rows(t);
-    Hq = static_cast<int>(t.size(1));
   } else if (a[15] != Py_None) {
     value_error("out_q without q");
   }
   const wp_rows kr = rows(k), vr = rows(v);
-  if (T > INT_MAX) value_error("too many tokens");
   run("wp_rope_append", [&] {
-    return f_rope_append(&q, &qo, Hq, &kr, &vr, static_cast<int>(Hkv), static_cast<int>(T), static_cast<int>(d), rot, index[0], index[1],
-                         index[2], c.k, c.layout, c.v, c.B, c.Lmax, c.block_table, c.max_pages, c.page_size, c.n_pages, theta, data(fs),
-                         scale_all, amplitude, layout, call.handle());
+    return f_rope_append(&q, &qo, Hq, &kr, &vr, Hkv, T, d, rot, index[0], index[1], index[2], c.k, c.layout, c.v, c.B, c.Lmax, c.block_table,
+                         c.max_pages, c.page_size, c.n_pages, theta, data(fs), scale_all, amplitude, layout, call.handle());
   });
   return a[0] == Py_None ? Py_NewRef(Py_None) : give(a[15], made);
   END_HANDLE_TH_ERRORS
@@ -372,7 +373,7 @@ PyObject *decode_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
   count(n, 14);
   const at::Tensor &q = tensor(a[0], "q", BF16, 4, -1);
   const int device = q.get_device();
-  const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2), d = q.size(3);
+  const int B = fit(q.size(0)), T = fit(q.size(1)), Hq = fit(q.size(2)), d = fit(q.size(3));
   const at::Tensor &lens = tensor(a[3], "lens", I32, 1, device);
   const at::Tensor &parents = tensor(a[4], "parents", I32, 2, device);
   if (lens.size(0) != B || parents.size(0) != B || parents.size(1) != T) value_error("lens must be [B] and parents [B, T]");
@@ -385,7 +386,6 @@ PyObject *decode_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const Cache c = cache(a[1], a[2], a[6], device, B, -1, d);
   const std::vector<int32_t> cut = cutoffs(a[7], d);
   const double scale = number(a[8]);
-  if (Hq > INT_MAX || T > INT_MAX) value_error("a size does not fit 32 bits");
   Call call(device, a[13]);
   at::Tensor made, made_lse;
   void *o;
@@ -409,14 +409,12 @@ PyObject *decode_tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
     lse = ptr<float>(made_lse);
   }
   const int64_t capacity = c.block_table == nullptr ? c.Lmax : static_cast<int64_t>(c.max_pages) * c.page_size;
-  const size_t need = capacity > INT_MAX ? 0
-                                         : f_decode_tree_workspace_bytes(static_cast<int>(B), static_cast<int>(T), static_cast<int>(Hq),
-                                                                         c.Hkv, static_cast<int>(d), static_cast<int>(capacity));
+  const size_t need = capacity > INT_MAX ? 0 : f_decode_tree_workspace_bytes(B, T, Hq, c.Hkv, d, static_cast<int>(capacity));
   Workspace ws(a[11], need, call);
   run("wp_decode_tree", [&] {
-    return f_decode_tree(q.data_ptr(), c.k, c.layout, c.v, ints(lens), ints(parents), nodes, static_cast<int>(T), c.Lmax, c.block_table,
-                         c.max_pages, c.page_size, c.n_pages, static_cast<int>(B), static_cast<int>(Hq), c.Hkv, static_cast<int>(d),
-                         data(cut), static_cast<float>(scale), o, lse, ws.data, ws.bytes, call.handle());
+    return f_decode_tree(q.data_ptr(), c.k, c.layout, c.v, ints(lens), ints(parents), nodes, T, c.Lmax, c.block_table, c.max_pages,
+                         c.page_size, c.n_pages, B, Hq, c.Hkv, d, data(cut), static_cast<float>(scale), o, lse, ws.data, ws.bytes,
+                         call.handle());
   });
   PyObject *r = PyTuple_New(2);
   PyTuple_SET_ITEM(r, 0, give(a[9], made));
@@ -447,9 +445,9 @@ PyObject *kv_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
     made = call.empty({B}, I32);
     out = ptr<int32_t>(made);
   }
-  if (path.size(1) > INT_MAX) value_error("a size does not fit 32 bits");
+  const int A = fit(path.size(1));
   run("wp_kv_compact", [&] {
-    return f_kv_compact(c.k, c.layout, c.v, ints(lens), ints(path), static_cast<int>(path.size(1)), ints(keep), out, c.Lmax, c.block_table,
+    return f_kv_compact(c.k, c.layout, c.v, ints(lens), ints(path), A, ints(keep), out, c.Lmax, c.block_table,
                         c.max_pages, c.page_size, c.n_pages, c.B, c.Hkv, c.d, call.handle());
   });
   return give(a[6], made);
@@ -463,7 +461,7 @@ PyObject *pages_update(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const at::Tensor &refs = tensor(a[0], "refs", I32, 1, -1);
   const int device = refs.get_device();
   const at::Tensor &bt = tensor(a[1], "block_table", I32, 2, device);
-  const int64_t pages = refs.size(0), B = bt.size(0), most = bt.size(1);
+  const int pages = fit(refs.size(0)), B = fit(bt.size(0)), most = fit(bt.size(1));
   const char *names[4] = {"lens", "parent", "keep", "new_lens"};
   const int32_t *in[4];
   for (int i = 0; i < 4; ++i) {
@@ -472,15 +470,13 @@ PyObject *pages_update(PyObject *, PyObject *const *a, Py_ssize_t n) {
     in[i] = ints(t);
   }
   const int page = integer(a[6], "page_size");
-  if (pages > INT_MAX || B > INT_MAX || most > INT_MAX) value_error("a size does not fit 32 bits");
   Call call(device, a[8]);
   const at::Tensor out[5] = {call.empty({pages}, I32), call.empty({B, most}, I32), call.empty({B}, I32), call.empty({B, 3}, I32),
                              call.empty({4}, I32)};
-  Workspace ws(a[7], f_pages_update_workspace_bytes(static_cast<int>(B), static_cast<int>(pages)), call);
+  Workspace ws(a[7], f_pages_update_workspace_bytes(B, pages), call);
   run("wp_pages_update", [&] {
     return f_pages_update(ints(refs), ints(bt), in[0], in[1], in[2], in[3], ptr<int32_t>(out[0]), ptr<int32_t>(out[1]), ptr<int32_t>(out[2]),
-                          ptr<int32_t>(out[3]), ptr<int32_t>(out[4]), static_cast<int>(B), static_cast<int>(most), page,
-                          static_cast<int>(pages), ws.data, ws.bytes, call.handle());
+                          ptr<int32_t>(out[3]), ptr<int32_t>(out[4]), B, most, page, pages, ws.data, ws.bytes, call.handle());
   });
   PyObject *r = PyTuple_New(5);
   for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(out[i]));

@@ -164,3 +164,20 @@ def test_pages_with_counts_near_32_bits(pool):
     less = [top - 1] + refs[1:]
     fork = update(less, [0, 0], [16, 16], [16, 16])
     assert fork[0][:2] == [top, 0] and fork[1] == [[0, -1], [0, -1]] and fork[4][0] == wp.PAGES_OK
+
+
+def test_sizes_that_do_not_fit_32_bits():
+    """A head of 2^32 + 128 dims is no head of 128, nor a block table of 2^32 + 1 rows one of a single row."""
+    x = torch.empty(1, 1, 1, 2 ** 32 + 128, dtype=torch.bfloat16, device="cuda")
+    for more in ({}, {"out_q": x}):
+        with pytest.raises(ValueError, match="32 bits"):
+            wp.wp_rope_qk(x, None, 1e4, wp.ROPE_INTERLEAVED, **more)
+    with pytest.raises(ValueError, match="32 bits"):
+        wp.wp_rope_append(None, x[0], x[0], x, x, _i32([0]), _i32([0]), _i32([0]), 1e4, wp.ROPE_INTERLEAVED)
+    del x
+    kv, rows = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.empty(2 ** 32 + 1, 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="32 bits"):
+        wp.wp_rope_append(None, rows, rows, kv, kv.clone(), _i32([0]), _i32([0]), _i32([0]), 1e4, wp.ROPE_INTERLEAVED, block_table=table)
+    del table
+    torch.cuda.empty_cache()
