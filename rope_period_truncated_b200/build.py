@@ -64,10 +64,9 @@ def _build_binding(force: bool, verbose: bool) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    _build_binding(force, verbose)
+def _build_library(force: bool, verbose: bool, extra_flags) -> None:
     if not force and not _stale():
-        return LIB
+        return
     nvcc = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-shared", *sources(), "-o", tmp]
@@ -75,6 +74,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """The library first: it needs no torch headers, and all calls but the serving ones need no binding."""
+    _build_library(force, verbose, extra_flags)
+    _build_binding(force, verbose)
     return LIB
 
 

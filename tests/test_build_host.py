@@ -1,0 +1,40 @@
+"""The build of the two shared objects, with the compilers faked: what is built
+when, and what is left when one of them fails. No GPU."""
+import os
+import subprocess
+
+import pytest
+
+from rope_period_truncated_b200 import build as wpbuild
+
+
+@pytest.fixture
+def compilers(tmp_path, monkeypatch):
+    """Build into an empty folder; returns the list of what was compiled, and the programs that are missing."""
+    monkeypatch.setattr(wpbuild, "LIB", str(tmp_path / "libwaveprune.so"))
+    monkeypatch.setattr(wpbuild, "BINDING", str(tmp_path / "_calls.so"))
+    built, missing = [], set()
+
+    def call(cmd, **_):
+        name = os.path.basename(cmd[0])
+        if name in missing:
+            raise FileNotFoundError(name)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write(name)
+        built.append(name)
+
+    monkeypatch.setattr(subprocess, "check_call", call)
+    return built, missing
+
+
+def test_library_is_built_where_the_binding_cannot_be(compilers):
+    built, missing = compilers
+    missing.add("g++")
+    with pytest.raises(FileNotFoundError):
+        wpbuild.build()
+    assert built == ["nvcc"] and os.path.exists(wpbuild.LIB) and not os.path.exists(wpbuild.BINDING)
+    missing.clear()
+    wpbuild.build()
+    assert built == ["nvcc", "g++"] and os.path.exists(wpbuild.BINDING)
+    wpbuild.build()
+    assert built == ["nvcc", "g++"]  # nothing has changed
