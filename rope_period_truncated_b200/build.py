@@ -45,11 +45,26 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def _build_binding(force: bool, verbose: bool) -> None:
+def _binding_stale(made_for: str) -> bool:
+    """Is the binding absent, older than its sources, or built against another torch or Python, whose ABI it would not fit?"""
+    if not os.path.exists(BINDING) or not os.path.exists(_binding_note()):
+        return True
+    with open(_binding_note()) as f:
+        if f.read() != made_for:
+            return True
     deps = (BINDING_SOURCE, os.path.join(INCLUDE, "waveprune.h"))
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
-        return
+    return any(os.path.getmtime(p) > os.path.getmtime(BINDING) for p in deps)
+
+
+def _binding_note() -> str:
+    return os.path.join(os.path.dirname(BINDING), "_build", "calls.txt")
+
+
+def _build_binding(force: bool, verbose: bool) -> None:
     import torch
+    made_for = f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}\n"
+    if not force and not _binding_stale(made_for):
+        return
     from torch.utils import cpp_extension
     include = [f for p in cpp_extension.include_paths("cuda") for f in ("-isystem", p)]
     libs = [f for p in cpp_extension.library_paths("cuda") for f in ("-L", p)]
@@ -62,6 +77,9 @@ def _build_binding(force: bool, verbose: bool) -> None:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(_binding_note()), exist_ok=True)
+    with open(_binding_note(), "w") as f:
+        f.write(made_for)
 
 
 def _build_library(force: bool, verbose: bool, extra_flags) -> None:

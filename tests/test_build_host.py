@@ -38,3 +38,27 @@ def test_library_is_built_where_the_binding_cannot_be(compilers):
     assert built == ["nvcc", "g++"] and os.path.exists(wpbuild.BINDING)
     wpbuild.build()
     assert built == ["nvcc", "g++"]  # nothing has changed
+
+
+def test_binding_of_another_torch_or_python_is_rebuilt(compilers, monkeypatch):
+    import sysconfig
+
+    import torch
+    built, _ = compilers
+    wpbuild.build()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    wpbuild.build()
+    assert built == ["nvcc", "g++", "g++"]
+    was = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399" if name == "SOABI" else was(name))
+    wpbuild.build()
+    wpbuild.build()
+    assert built == ["nvcc"] + 3 * ["g++"]
+
+
+def test_binding_of_unknown_origin_is_rebuilt(compilers):
+    built, _ = compilers
+    for path in (wpbuild.LIB, wpbuild.BINDING):
+        open(path, "w").close()
+    wpbuild.build()
+    assert built == ["g++"]
