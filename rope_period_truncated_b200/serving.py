@@ -17,6 +17,7 @@ are allocated on ``stream`` and may be used and dropped on the current one.
 from __future__ import annotations
 
 import ctypes
+import os
 from array import array
 
 import numpy as np
@@ -71,7 +72,9 @@ class _Native:
         try:
             from . import _calls
         except ImportError as e:
-            raise ImportError("_calls.so not built; run python -m rope_period_truncated_b200.build") from e
+            from . import build
+            why = f"does not load ({e})" if os.path.exists(build.BINDING) else "not built"
+            raise ImportError(f"_calls.so {why}; run python -m rope_period_truncated_b200.build --force") from e
         _calls.connect({f: ctypes.cast(getattr(lib, f), P).value for f in DEVICE_CALLS}, WavePruneError)
         for f in ("rope_qk", "rope_append", "decode_tree", "kv_compact", "pages_update", "pages_copy"):
             setattr(self, f, getattr(_calls, f))

@@ -62,3 +62,21 @@ def test_binding_of_unknown_origin_is_rebuilt(compilers):
         open(path, "w").close()
     wpbuild.build()
     assert built == ["g++"]
+
+
+def test_import_errors_say_what_is_wrong(monkeypatch, tmp_path):
+    """A binding that is not there is to be built; one that does not load says why."""
+    import sys
+
+    import rope_period_truncated_b200 as wp
+    from rope_period_truncated_b200 import serving
+
+    monkeypatch.setitem(sys.modules, "rope_period_truncated_b200._calls", None)  # the import fails
+    monkeypatch.delattr(wp, "_calls", raising=False)
+    monkeypatch.setattr(wpbuild, "BINDING", str(tmp_path / "_calls.so"))
+    with pytest.raises(ImportError, match="not built"):
+        serving._Native().rope_qk
+    open(wpbuild.BINDING, "w").close()
+    with pytest.raises(ImportError, match="does not load.*_calls") as e:
+        serving._Native().rope_qk
+    assert "not built" not in str(e.value) and isinstance(e.value.__cause__, ImportError)
