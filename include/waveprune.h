@@ -456,6 +456,9 @@ int wp_cutoffs_partial(int d_h, int rot_dim, double theta, const double *freq_sc
  *   rot_dim      multiple of 16, 16..1024; freq_scale out [rot_dim/2].
  *   factor >= 1, original_len > 0, 0 <= turns_slow < turns_fast (1 and 32 are
  *   usual).
+ * The ramp is linear in the number of turns. A checkpoint whose ramp is linear
+ * in the channel's index between two rounded channels (also in use with 1 and
+ * 32) has other scales in between: pass those as freq_scale instead.
  * The cutoffs follow the scaled frequencies: pass the same freq_scale to
  * wp_cutoffs / wp_cutoffs_partial. Errors: WP_ERR_ARG.
  */
@@ -561,6 +564,8 @@ size_t wp_decode_tree_workspace_bytes(int B, int T, int H_q, int H_kv, int d_h, 
  *                contents on entry do not matter. Calls that may run at the
  *                same time need workspaces of their own.
  * o, lse and the workspace overlap nothing else.
+ * The softmax is fp32; its weights round to bf16 for the product with V (2^-8 of
+ * each, as in wp_prefill and wp_decode), O rounds to bf16 once.
  * A sequence whose length, node count, parents or pages are out of range gets
  * NaN rows (nothing is read through them). A wait that gives up records
  * WP_ERR_TIMEOUT (wp_device_status) and gives NaN rows.

@@ -30,8 +30,9 @@ namespace cg = cooperative_groups;
 // One cluster of up to 8 blocks does it all: its steps are ordered by the
 // hardware's cluster barrier instead of by launches or by waiting on flags. It
 // is a chain of a dozen dependent memory accesses and four barriers, so its
-// time is latency (256 rows, a pool of 40000 pages: 20 us): few steps, and no
-// more blocks than have work.
+// time is latency (256 rows, a pool of 40000 pages: 21 us, with the scratch of 8
+// blocks in global memory, where every atomic and dependent read goes to L2): few
+// steps, and no more blocks than have work.
 constexpr int PG_THREADS = 1024;
 constexpr int MAX_CLUSTER = 8;
 constexpr int ONE_BLOCK = 8192;  // fewer pages and table entries: one block, its scratch in shared memory
@@ -402,9 +403,9 @@ __global__ void __launch_bounds__(COMPACT_THREADS) compact_kernel(const __grid_c
 
 cudaError_t launch_pages_update(PagesArgs a, cudaStream_t stream) {
   // one block with its scratch in shared memory (24 bytes a page, 8 a row) while
-  // that holds it, else one per 4096 pages and table entries, up to the portable
-  // cluster size. 64 rows of 40 pages, a pool of 5000: 11.8 us with one block,
-  // 14.6 with two and the scratch in memory.
+  // that holds it, else four from 8192 pages and table entries on and eight, the
+  // portable cluster size, from 16384. 64 rows of 40 pages, a pool of 5000: 11.8 us
+  // with one block, 14.6 with two that have their scratch in memory.
   const int64_t work = a.n_pages + static_cast<int64_t>(a.B) * a.max_pages;
   int blocks = 1;
   while (work >= ONE_BLOCK && blocks < MAX_CLUSTER && blocks <= work / PER_BLOCK) blocks *= 2;

@@ -170,8 +170,8 @@ struct TreeArgs {
 // tile about 1). More rows go to the one that has query rows there: tiles of
 // whole nodes, 64 keys, two CTAs per SM, each
 // (sequence, KV head) split on its own: so that the CTAs fill the SMs once (all
-// 296 places where a CTA then has at least 1024 keys: 252 rows over 128K keys
-// 146 us, 159 with 256 CTAs; else 256, with less to merge: 4 x 2.5K to 4K keys
+// 296 places where a CTA then has at least 1024 keys: 252 rows over 128K keys,
+// back to back, 146 us, 159 with 256 CTAs; else 256, with less to merge: 4 x 2.5K to 4K keys
 // 30.7 us with 9 splits, 28.4 with 8), or,
 // for several sequences, whose lengths may differ, up to twice as long as a CTA
 // keeps 1024 keys (16 x 16K to 32K keys, 64 rows: 248 us, 261 with twice as many).

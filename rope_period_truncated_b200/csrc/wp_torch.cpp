@@ -3,8 +3,8 @@
 // C ABI, whose function addresses the package hands over. These calls last a
 // few microseconds on the device at their smallest, so their marshalling is
 // compiled. Measured, us a call among others, here / marshalled in Python: a
-// rotation of 256 tokens 6.0 / 15, an append of 128 tokens 6.0 / 18, an append
-// with a compaction 10 / 30, a page step of two calls 11 / 25.
+// rotation of 256 tokens 5.6 / 15, an append of 128 tokens 5.7 / 18, an append
+// with a compaction 9.2 / 30, a page step of two calls 10.3 / 25.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -22,7 +22,10 @@
 //             for both was what bounded the kernel: issuing a sub-tile's 12
 //             products and their commits took it about 1800 cycles.
 //   warps 0-3 softmax, a row per thread, online in base 2; O is rescaled only
-//             when a maximum grows by more than 2^8.
+//             when a maximum grows by more than 2^8. P rounds to bf16 (2^-8 of
+//             each weight, as in the package's prefill and decode): both
+//             operands of a product have one type, and V is bf16. Maxima, sums,
+//             O and partial results are fp32; the sums take P unrounded.
 // Groups whose cutoff falls inside a sub-tile's distances go first, one cutoff
 // at a time in ascending order, and S is masked in place after each (windows
 // of ascending cutoffs are nested, so later masks keep what earlier ones did).
@@ -35,14 +38,20 @@
 // Splits write O (fp32) and LSE to the workspace; a second kernel merges them
 // (4 to 7 us; merging in a cluster through its shared memory took 7 and more).
 //
-// What bounds it. Few splits of short caches: latency, about 3 us until the
-// first keys are there and 2 from the last product to the written rows (4
-// sequences of 2.5K to 4K keys, 64 rows: 25 us, of which the merge 4). 16
-// sequences of 16K to 32K keys, 64 rows: 241 us, 5.1 TB/s. 252 rows over 128K
-// keys, most groups live: 146 us, 600 TFLOP/s, a sub-tile in about 1760 cycles
-// per CTA: its products take 640 of the tensor core's (those of S at two thirds
-// of the rate, since each re-reads its 4 KB of Q from shared memory), those of
-// the SM's other CTA as many, and P V(u) to S(u + 2) to P(u + 2) is a chain.
+// What bounds it. Short caches: latency. 4 sequences of 2.5K to 4K keys, 64
+// rows: 25 us a call. By length (4 x 512, 1K, 2K, 4K, 8K keys: 15.5, 16.4, 19.2,
+// 23.7, 35 us) a CTA's eighth of 4K keys, 8 sub-tiles one after the other, is 9
+// us of that (1.1 us each, from 8K keys on 1.4); launches, first keys, last rows
+// and the merge are 11, the partial rows of 8 splits instead of 2 about 4. 16
+// sequences of 16K to 32K keys, 64 rows: 245 us, 5.1 TB/s. 252 rows over 128K
+// keys, most groups live: 143 us back to back (612 TFLOP/s), 170 us a call among
+// calls on other inputs; no pipe is full (tensor 33 %, XU 50 %, DRAM 33 %), a
+// sub-tile takes about 1760 cycles per CTA: P V(u) to S(u + 2) to P(u + 2) is a
+// chain through two issuers and their barriers, and the two row tiles of a KV
+// head run as separate CTAs that each load all keys (one of them from L2). wp_prefill.cu runs products
+// of the same shape at 980 TFLOP/s with two row tiles on one K/V stage, one
+// issuer per tile whose order spares those barriers, and part of the exponentials
+// on the FMA pipe; that arrangement has not been built here.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>

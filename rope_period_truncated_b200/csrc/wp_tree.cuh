@@ -124,7 +124,7 @@ __device__ __forceinline__ Place place_of(const CacheGeom &g, int b, int key, in
 // cycles, whatever its size, so where a tile is one box high a run of groups
 // goes in boxes of 4, 2 and 1. The loops stay rolled: a CTA's warps run five
 // different loops at a time, and unrolled ones do not fit the instruction cache
-// (16 sequences of 16K to 32K keys in pages of 32, 32 rows: 259 us unrolled, 224
+// (16 sequences of 16K to 32K keys in pages of 32, 32 rows: 259 us unrolled, 222
 // rolled).
 template <int D, bool KGM, int TILE>
 __device__ __forceinline__ void issue_k(const TreeMaps &tm, const Place &here, int have, uint32_t need, int box, int hk,

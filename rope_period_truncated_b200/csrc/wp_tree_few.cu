@@ -9,17 +9,21 @@
 // the four warps share a tile's exponentials evenly.
 //
 // What bounds it: HBM over long caches (16 sequences of 16K to 32K keys, 32 rows,
-// pages of 64 keys: 211 us, 5.9 TB/s; K in rows, whose 64-dim chunks are read
-// whole, 256), the issue of the copies where pages are small (32 keys 221 us, 16
-// keys 341), latency over short ones (4 sequences of 2.5K to 4K keys: 27 us; one
-// of 200 keys, a CTA per KV head: 9).
+// pages of 64 keys: 211 us back to back, 5.9 TB/s, 218 us a call among calls on
+// other inputs; K in rows, whose 64-dim chunks are read whole, 258), the issue of
+// the copies from one lane where pages of group-major K are small (32 keys 222
+// us, 16 keys 342), latency over short ones (4 sequences of 2.5K to 4K keys: 26
+// us; one of 200 keys, a CTA per KV head: 9, with 8 heads of 128 11). One
+// sequence of 128K keys, 32 rows: 81 us back to back where its bytes take 63; some
+// 10 of the 18 between are what a short call takes, the rest was not taken apart.
 //
 // One CTA per SM. All (sequence, KV head) units lie end to end as a line of
 // 128-key tiles, cut evenly among the CTAs, whatever the lengths: a CTA walks
 // over its stretch in segments (what of one unit falls into it), and its loads
 // run ahead across them. Warps 8 and 9 fetch K, and Q and V, warp 10 issues S^T
 // (M = 128 keys, N = rows, one K = 16 product per live group), warps 0-3 turn it
-// into P^T for the even tiles and warps 4-7 for the odd ones (bf16, in shared
+// into P^T for the even tiles and warps 4-7 for the odd ones (bf16, since V is: 2^-8
+// of each weight, as in the package's prefill; the sums take it unrounded; in shared
 // memory: B of the second product, rows contiguous), warp 11 issues O^T (M = 128
 // dims, V read as it lies, MN-major). Even and odd tiles have maxima, sums and
 // an O^T of their own: a softmax warp alone on its scheduler waits for its own
